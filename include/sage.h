@@ -30,6 +30,13 @@
  *   sage_attn_decode     paged FP8-KV decode (same page: window-family
  *                        workload, per-token FP8 K/V scales, MTP, GQA).
  *   sage_attn_decode_mxfp4  the same decode over an MXFP4 KV cache.
+ * A serving step over the paged cache, in call order:
+ *   sage_page_plan       pages, block tables and slots from the requests'
+ *                        lengths.
+ *   sage_kv_append, sage_kv_append_mxfp4  the new tokens' K and V quantised
+ *                        into their slots.
+ *   sage_attn_decode_shared, sage_attn_decode_shared_mxfp4  the decode for a
+ *                        batch whose sequences begin with the same prefix.
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers on the device that is current
@@ -362,6 +369,126 @@ sage_status sage_attn_decode_mxfp4(sage_hadamard h, sage_cview4 q_bf16, const ui
                                    uint8_t* q8_out, float* q_scale_out, void* ws, size_t ws_bytes,
                                    void* stream);
 
+/* Bytes of device workspace sage_attn_decode_shared and its MXFP4 form need
+ * on the current device: the partials of the prefix's and of the sequences'
+ * own keys. No initial contents are required; concurrent calls need distinct
+ * workspaces. */
+size_t sage_attn_decode_shared_workspace(int B, int T, int H, int Hk, int D);
+
+/* sage_attn_decode for a batch whose sequences begin with the same tokens
+ * (a system prompt, a document asked about many times): the shared tokens'
+ * keys and values are read and multiplied once for the query rows of all
+ * sequences instead of once per sequence.
+ *   prefix_len: DEVICE pointer to one int32, the shared tokens L (any
+ *   number, 0 included; read when the kernels run, so a captured graph
+ *   follows it); prefix_table: int32 [max_prefix_pages], the physical pages
+ *   of tokens 0 .. L - 1.
+ *   page_table, ctx_lens: as for sage_attn_decode, counted from the
+ *   sequence's first token: ctx includes the prefix, and entry e of a row is
+ *   the page of tokens e * page_size ... (entries wholly below L are not
+ *   read). A sequence may end inside the prefix (its rows see the prefix's
+ *   keys up to their own position) or be empty (ctx 0, a padded batch: its
+ *   rows are written as zeros).
+ * The computation is that of sage_attn_decode on the sequence [prefix's
+ * tokens 0 .. L - 1, own tokens L .. ctx - 1], windows included; the partial
+ * results of the two parts are combined in fp32 (log-sum-exp). The other
+ * arguments, cache formats, limits and errors are sage_attn_decode's; also
+ * UNSUPPORTED: B * Hk > 65535, B * T * H or a table of 2^31 or more tokens.
+ * A prefix_len outside [0, max_prefix_pages * page_size] is clamped and
+ * reported by sage_device_error like an out-of-range ctx. ws: at least
+ * sage_attn_decode_shared_workspace(...) bytes, 16-byte aligned. */
+sage_status sage_attn_decode_shared(sage_hadamard h, sage_cview4 q_bf16, const uint8_t* k_cache,
+                                    const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                                    const int32_t* prefix_table, int max_prefix_pages,
+                                    const int32_t* prefix_len, const int32_t* page_table,
+                                    const int32_t* ctx_lens, int B, int T, int H, int Hk, int D,
+                                    int page_size, int max_pages, int num_pages, int window,
+                                    float softmax_scale, int kv_flags, sage_view4 out_bf16, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/* sage_attn_decode_shared over an MXFP4 cache (sage_attn_decode_mxfp4's
+ * layouts and limits). */
+sage_status sage_attn_decode_shared_mxfp4(sage_hadamard h, sage_cview4 q_bf16, const uint8_t* k_cache,
+                                          const uint8_t* v_cache, const uint8_t* k_sf, const uint8_t* v_sf,
+                                          const int32_t* prefix_table, int max_prefix_pages,
+                                          const int32_t* prefix_len, const int32_t* page_table,
+                                          const int32_t* ctx_lens, int B, int T, int H, int Hk, int D,
+                                          int page_size, int max_pages, int num_pages, int window,
+                                          float softmax_scale, sage_view4 out_bf16, void* ws,
+                                          size_t ws_bytes, void* stream);
+
+/* One serving step's bookkeeping of the paged cache, on the device: pages
+ * taken from and given back to a free list, block tables, and the slots of
+ * the step's new tokens. All arrays int32.
+ *   cached_lens [B]: tokens request b has in the cache; new_lens [B]: tokens
+ *   it adds (0: none; negative: the request has ended and gives its pages
+ *   back). prefix_table [prefix_pages] (NULL and 0 without one): the whole
+ *   pages that every request of the batch stands on, P = prefix_pages *
+ *   page_size tokens. free_list [num_pages]: a stack of *free_count unused
+ *   pages.
+ * With start_b = P if cached_b = 0 and new_b > 0 (a request that joins), else
+ * cached_b; ctx_b = start_b + new_b (0 for one that has ended); held_b =
+ * ceil(start_b / page_size):
+ *   - the entries prefix_pages .. held_b - 1 of the requests that have ended
+ *     are pushed on the stack in request order, then every other request's
+ *     ceil(ctx_b / page_size) - held_b new pages are popped from its top in
+ *     request order and become its entries held_b, held_b + 1, ...;
+ *   - a joining request's first prefix_pages entries become prefix_table;
+ *   - the new tokens are numbered in request order: token_offsets [B + 1]
+ *     receives the exclusive sums of the new lengths, slot_map [max_tokens]
+ *     token t's slot = page * page_size + position % page_size, and -1 from
+ *     the last token on.
+ * Written: those entries of page_table [B, max_pages] alone; ctx_lens [B];
+ * *free_count_out; free_list's entries *free_count .. *free_count_out - 1
+ * (when pages are left over from those given back); token_offsets; slot_map.
+ * ctx_lens may be cached_lens and free_count_out may be free_count; no other
+ * two arrays may overlap.
+ * All or nothing: when the pages or the slots do not suffice, when a length
+ * is negative, exceeds max_pages * page_size or lies inside the prefix
+ * (0 < cached < P), or *free_count is not in [0, num_pages], the step changes
+ * no table or list, copies the lengths and the count, sets every slot to -1
+ * and every offset to 0, and sage_device_error reports INVALID_ARG (kernel
+ * SAGE_KERNEL_PLAN). page_size in {16, 32, 64, 128}, B <= 8192, max_tokens
+ * >= 0 (UNSUPPORTED beyond; also num_pages or max_pages * page_size >= 2^31).
+ * One launch; two when max_tokens > 65536. */
+sage_status sage_page_plan(const int32_t* cached_lens, const int32_t* new_lens, const int32_t* prefix_table,
+                           int prefix_pages, int32_t* free_list, const int32_t* free_count, int B,
+                           int max_pages, int page_size, int num_pages, int max_tokens, int32_t* page_table,
+                           int32_t* ctx_lens, int32_t* free_count_out, int32_t* token_offsets,
+                           int32_t* slot_map, void* stream);
+
+/* Write new tokens into the paged FP8 cache that sage_attn_decode reads.
+ *   k_bf16, v_bf16: [1, N, Hk, D] bf16 views of any strides, D the handle's;
+ *   N = 0 is a step without new tokens (nothing is launched);
+ *   k_mean: fp32 [Hk, D], 16-byte aligned, subtracted from every key, or
+ *   NULL (softmax does not see a constant key offset, so the tokens that are
+ *   attended together need the same mean and the decode needs none);
+ *   slot_map: int32 [N], token n's slot page * page_size + offset; a negative
+ *   slot skips its token; a slot >= num_pages * page_size is skipped and
+ *   reported by sage_device_error as INVALID_ARG (kernel SAGE_KERNEL_APPEND).
+ *   Slots of one call must differ: of tokens that share one, which one's
+ *   codes and scales stay is not specified.
+ * Per token and head: x = butterfly(K - k_mean) for K, x = V for V;
+ * a = max|x|, scale = a / 448, code = e4m3_rn_sat(x * (448 / a)) (a = 0:
+ * scale 0 and zero codes), written to k_scale / v_scale [num_pages, Hk,
+ * page_size]. With SAGE_KV_PER_TENSOR_SCALES k_scale / v_scale point to one
+ * positive fp32 each, which is read: code = e4m3_rn_sat(x * (1 / scale)).
+ * Caches and SAGE_KV_V_TRANSPOSED as for sage_attn_decode, 16-byte aligned.
+ * Nothing but the slots' own bytes is written. */
+sage_status sage_kv_append(sage_hadamard h, sage_cview4 k_bf16, sage_cview4 v_bf16, const float* k_mean,
+                           const int32_t* slot_map, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
+                           float* v_scale, int page_size, int num_pages, int kv_flags, void* stream);
+
+/* sage_kv_append into the MXFP4 cache that sage_attn_decode_mxfp4 reads (D =
+ * 128): per 32 consecutive elements a = max|x|, E = floor(log2 a) - 2 clamped
+ * to [-127, 125] (-127 for a = 0 or subnormal), codes E2M1(x * 2^-E) rounded
+ * to nearest even and saturating, scale byte E + 127 (sage_quant_qk_mx's
+ * block format). */
+sage_status sage_kv_append_mxfp4(sage_hadamard h, sage_cview4 k_bf16, sage_cview4 v_bf16,
+                                 const float* k_mean, const int32_t* slot_map, uint8_t* k_cache,
+                                 uint8_t* v_cache, uint8_t* k_sf, uint8_t* v_sf, int page_size,
+                                 int num_pages, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* sage_status_string(sage_status s);
 
@@ -379,6 +506,8 @@ sage_status sage_device_error(void* stream);
 #define SAGE_KERNEL_DECODE 2
 #define SAGE_KERNEL_PROBE 3
 #define SAGE_KERNEL_ATTN_MX 4
+#define SAGE_KERNEL_PLAN 5
+#define SAGE_KERNEL_APPEND 6
 
 /* sage_device_error, also saying where the reported error was recorded:
  * *kernel receives a SAGE_KERNEL_* id (0 with SAGE_OK), *site the number of

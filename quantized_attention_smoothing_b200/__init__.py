@@ -33,12 +33,16 @@ EXPORTS = (
     "sage_attn_fwd_workspace", "sage_attn_fwd", "sage_attn_fwd_q16", "sage_attn_decode_workspace",
     "sage_attn_decode", "sage_status_string", "sage_device_error", "sage_device_error_where",
     "sage_wait_probe", "sage_quant_qk_mx", "sage_attn_fwd_mx", "sage_attn_decode_mxfp4",
+    "sage_attn_decode_shared_workspace", "sage_attn_decode_shared", "sage_attn_decode_shared_mxfp4",
+    "sage_page_plan", "sage_kv_append", "sage_kv_append_mxfp4",
 )
 
 SAGE_KERNEL_ATTN = 1
 SAGE_KERNEL_DECODE = 2
 SAGE_KERNEL_PROBE = 3
 SAGE_KERNEL_ATTN_MX = 4
+SAGE_KERNEL_PLAN = 5
+SAGE_KERNEL_APPEND = 6
 SAGE_KV_PER_TENSOR_SCALES = 1
 SAGE_KV_V_TRANSPOSED = 2
 
@@ -110,6 +114,20 @@ def lib():
     L.sage_attn_decode_mxfp4.restype = i32
     L.sage_attn_decode_mxfp4.argtypes = [vp, CView4, vp, vp, vp, vp, vp, vp] + [i32] * 9 + \
         [f32, View4, vp, vp, vp, sz, vp]
+    L.sage_attn_decode_shared_workspace.restype = sz
+    L.sage_attn_decode_shared_workspace.argtypes = [i32] * 5
+    L.sage_attn_decode_shared.restype = i32
+    L.sage_attn_decode_shared.argtypes = [vp, CView4] + [vp] * 5 + [i32, vp, vp, vp] + [i32] * 9 + \
+        [f32, i32, View4, vp, sz, vp]
+    L.sage_attn_decode_shared_mxfp4.restype = i32
+    L.sage_attn_decode_shared_mxfp4.argtypes = [vp, CView4] + [vp] * 5 + [i32, vp, vp, vp] + [i32] * 9 + \
+        [f32, View4, vp, sz, vp]
+    L.sage_page_plan.restype = i32
+    L.sage_page_plan.argtypes = [vp, vp, vp, i32, vp, vp] + [i32] * 5 + [vp] * 6
+    L.sage_kv_append.restype = i32
+    L.sage_kv_append.argtypes = [vp, CView4, CView4] + [vp] * 6 + [i32] * 3 + [vp]
+    L.sage_kv_append_mxfp4.restype = i32
+    L.sage_kv_append_mxfp4.argtypes = [vp, CView4, CView4] + [vp] * 6 + [i32] * 2 + [vp]
     L.sage_device_error.restype = i32
     L.sage_device_error.argtypes = [vp]
     L.sage_device_error_where.restype = i32
@@ -310,6 +328,95 @@ def sage_attn_decode_mxfp4(h, q, k_cache, v_cache, k_sf, v_sf, page_table, ctx_l
                                         _ptr(q8_out), _ptr(q_scale_out), _ptr(ws),
                                         0 if ws is None else ws.numel() * ws.element_size(),
                                         _stream(stream)), "sage_attn_decode_mxfp4")
+
+
+def sage_attn_decode_shared_workspace(B, T, H, Hk, D):
+    return int(lib().sage_attn_decode_shared_workspace(B, T, H, Hk, D))
+
+
+def _shared_ws(q, Hk, ws):
+    if ws is None:
+        B, T, H, D = q.shape
+        ws = torch.empty((sage_attn_decode_shared_workspace(B, T, H, Hk, D),), dtype=torch.uint8,
+                         device=q.device)
+    return ws
+
+
+def sage_attn_decode_shared(h, q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_len,
+                            page_table, ctx_lens, page_size, num_pages, window, softmax_scale, out,
+                            ws=None, stream=None, kv_flags=0):
+    """sage_attn_decode for a batch whose sequences begin with the same tokens:
+    prefix_table int32 [pages] and prefix_len int32 [1] (both on the GPU)
+    give the shared tokens' pages, page_table [B, max_pages] and ctx_lens
+    count from the sequence's first token as in sage_attn_decode."""
+    B, T, H, D = q.shape
+    Hk = k_cache.shape[1]
+    ws = _shared_ws(q, Hk, ws)
+    _check(lib().sage_attn_decode_shared(h.handle, _view(q, CView4), _ptr(k_cache), _ptr(v_cache),
+                                         _ptr(k_scale), _ptr(v_scale), _ptr(prefix_table),
+                                         prefix_table.numel(), _ptr(prefix_len), _ptr(page_table),
+                                         _ptr(ctx_lens), B, T, H, Hk, D, int(page_size),
+                                         int(page_table.shape[1]), int(num_pages), int(window),
+                                         float(softmax_scale), int(kv_flags), _view(out, View4), _ptr(ws),
+                                         ws.numel() * ws.element_size(), _stream(stream)),
+           "sage_attn_decode_shared")
+
+
+def sage_attn_decode_shared_mxfp4(h, q, k_cache, v_cache, k_sf, v_sf, prefix_table, prefix_len,
+                                  page_table, ctx_lens, page_size, num_pages, window, softmax_scale,
+                                  out, ws=None, stream=None):
+    """sage_attn_decode_shared over an MXFP4 cache (the layouts of
+    sage_attn_decode_mxfp4)."""
+    B, T, H, D = q.shape
+    Hk = k_cache.shape[1]
+    ws = _shared_ws(q, Hk, ws)
+    _check(lib().sage_attn_decode_shared_mxfp4(h.handle, _view(q, CView4), _ptr(k_cache), _ptr(v_cache),
+                                               _ptr(k_sf), _ptr(v_sf), _ptr(prefix_table),
+                                               prefix_table.numel(), _ptr(prefix_len), _ptr(page_table),
+                                               _ptr(ctx_lens), B, T, H, Hk, D, int(page_size),
+                                               int(page_table.shape[1]), int(num_pages), int(window),
+                                               float(softmax_scale), _view(out, View4), _ptr(ws),
+                                               ws.numel() * ws.element_size(), _stream(stream)),
+           "sage_attn_decode_shared_mxfp4")
+
+
+def sage_page_plan(cached_lens, new_lens, free_list, free_count, page_size, page_table, ctx_lens,
+                   free_count_out, token_offsets, slot_map, prefix_table=None, stream=None):
+    """Block tables, the free list and the new tokens' slots of one serving
+    step (all int32 tensors; ctx_lens may be cached_lens and free_count_out
+    free_count)."""
+    B, max_pages = page_table.shape
+    _check(lib().sage_page_plan(_ptr(cached_lens), _ptr(new_lens), _ptr(prefix_table),
+                                0 if prefix_table is None else prefix_table.numel(), _ptr(free_list),
+                                _ptr(free_count), B, max_pages, int(page_size), free_list.numel(),
+                                0 if slot_map is None else slot_map.numel(), _ptr(page_table),
+                                _ptr(ctx_lens), _ptr(free_count_out), _ptr(token_offsets),
+                                _ptr(slot_map), _stream(stream)), "sage_page_plan")
+
+
+def _tokens_view(t):
+    """[N, Hk, D] as the [1, N, Hk, D] view of the C ABI."""
+    if t.dim() != 3:
+        raise ValueError("expected [tokens, heads, head size], got shape %s" % (tuple(t.shape),))
+    return _view(t.unsqueeze(0), CView4)
+
+
+def sage_kv_append(h, k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_mean=None, kv_flags=0,
+                   stream=None):
+    """Quantise the new tokens' k and v ([N, Hk, D] bf16 views) into an FP8
+    cache at slot_map (int32 [N]; a negative slot skips its token)."""
+    _check(lib().sage_kv_append(h.handle, _tokens_view(k), _tokens_view(v), _ptr(k_mean), _ptr(slot_map),
+                                _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                int(k_cache.shape[2]), int(k_cache.shape[0]), int(kv_flags),
+                                _stream(stream)), "sage_kv_append")
+
+
+def sage_kv_append_mxfp4(h, k, v, slot_map, k_cache, v_cache, k_sf, v_sf, k_mean=None, stream=None):
+    """sage_kv_append into an MXFP4 cache (the layouts of sage_attn_decode_mxfp4)."""
+    _check(lib().sage_kv_append_mxfp4(h.handle, _tokens_view(k), _tokens_view(v), _ptr(k_mean),
+                                      _ptr(slot_map), _ptr(k_cache), _ptr(v_cache), _ptr(k_sf), _ptr(v_sf),
+                                      int(k_cache.shape[2]), int(k_cache.shape[0]), _stream(stream)),
+           "sage_kv_append_mxfp4")
 
 
 def sage_quant_qk_mx(h, q, k, q4, q_sf, k4, k_sf, k_mean=None, ws=None, stream=None):

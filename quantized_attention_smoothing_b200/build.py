@@ -27,6 +27,8 @@ SOURCES = {
     "attn_fwd.cu": [],
     "attn_mx.cu": [],
     "decode.cu": [],
+    "plan.cu": [],
+    "append.cu": ["-fmad=false"],
     "sage_api.cu": [],
     "probe.cu": [],
 }

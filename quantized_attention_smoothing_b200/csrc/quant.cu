@@ -476,22 +476,6 @@ __device__ __forceinline__ uint2 codes8_clamp(const uint64_t (&x2)[N], int k0, f
     return make_uint2(w[0], w[1]);
 }
 
-// Eight E2M1 codes (round to nearest even, saturating) of the four value
-// pairs, element 2i in the low nibble of byte i.
-__device__ __forceinline__ uint32_t e2m1x8(uint64_t a, uint64_t b, uint64_t c, uint64_t d) {
-    uint32_t w;
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
-        : "=r"(w)
-        : "f"(p2lo(a)), "f"(p2hi(a)), "f"(p2lo(b)), "f"(p2hi(b)), "f"(p2lo(c)), "f"(p2hi(c)),
-          "f"(p2lo(d)), "f"(p2hi(d)));
-    return w;
-}
-
 // ---------------------------------------------------------------- kernel
 // Persistent CTAs of 512 threads; CTA c takes tiles c, c + G, c + 2G, ...
 // (G = gridDim.x, odd when K and V alternate, so every CTA gets both

@@ -126,5 +126,21 @@ __device__ __forceinline__ uint4 row_codes16(const uint64_t (&x2)[D / 2], float 
     return make_uint4(w4[0], w4[1], w4[2], w4[3]);
 }
 
+// Eight E2M1 codes (round to nearest even, saturating) of the four value
+// pairs, element 2i in the low nibble of byte i.
+__device__ __forceinline__ uint32_t e2m1x8(uint64_t a, uint64_t b, uint64_t c, uint64_t d) {
+    uint32_t w;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(w)
+        : "f"(p2lo(a)), "f"(p2hi(a)), "f"(p2lo(b)), "f"(p2hi(b)), "f"(p2lo(c)), "f"(p2hi(c)),
+          "f"(p2lo(d)), "f"(p2hi(d)));
+    return w;
+}
+
 }  // namespace qrow
 }  // namespace sage

@@ -78,7 +78,7 @@ sage_status decode_args(sage_hadamard h, sage_cview4 q_bf16, const int32_t* page
                         const int32_t* ctx_lens, int B, int T, int H, int Hk, int D, int page_size,
                         int max_pages, int num_pages, int window, float softmax_scale,
                         sage_view4 out_bf16, uint8_t* q8_out, float* q_scale_out, void* ws,
-                        size_t ws_bytes, sage::DecodeArgs* a) {
+                        size_t ws_bytes, sage::DecodeArgs* a, bool shared = false) {
     if (!h || !q_bf16.ptr || !page_table || !ctx_lens || !out_bf16.ptr) return SAGE_ERR_INVALID_ARG;
     if (B < 1 || T < 1 || H < 1 || Hk < 1 || D < 1 || page_size < 1 || max_pages < 1 ||
         num_pages < 1 || window < 1 || !std::isfinite(softmax_scale))
@@ -97,7 +97,8 @@ sage_status decode_args(sage_hadamard h, sage_cview4 q_bf16, const int32_t* page
     if (!aligned(page_table, 4) || !aligned(ctx_lens, 4) || !aligned(q_bf16.ptr, 2) ||
         !aligned(out_bf16.ptr, 2) || !aligned(q8_out, 16) || !aligned(q_scale_out, 4))
         return SAGE_ERR_ALIGNMENT;
-    const size_t need = sage::decode_ws_bytes(B, T, H, Hk, D, window);
+    const size_t need = shared ? sage::decode_shared_ws_bytes(B, T, H, Hk, D)
+                               : sage::decode_ws_bytes(B, T, H, Hk, D, window);
     if (need > 0 && (!ws || ws_bytes < need)) return SAGE_ERR_WORKSPACE;
     if (!aligned(ws, 16)) return SAGE_ERR_ALIGNMENT;
     int dev = -1;
@@ -124,6 +125,60 @@ sage_status decode_args(sage_hadamard h, sage_cview4 q_bf16, const int32_t* page
     return SAGE_OK;
 }
 
+// The checks of sage_attn_decode_shared and its MXFP4 form beyond decode_args.
+sage_status shared_args(const int32_t* prefix_table, int max_prefix_pages, const int32_t* prefix_len, int B,
+                        int T, int H, int Hk, int page_size, int max_pages, sage::DecodeSharedArgs* a) {
+    if (!prefix_table || !prefix_len || max_prefix_pages < 1) return SAGE_ERR_INVALID_ARG;
+    if ((int64_t)max_prefix_pages * page_size >= (int64_t(1) << 31) ||
+        (int64_t)max_pages * page_size >= (int64_t(1) << 31) || (int64_t)B * T * H >= (int64_t(1) << 31) ||
+        (int64_t)B * Hk > 65535)
+        return SAGE_ERR_UNSUPPORTED;
+    if (!aligned(prefix_table, 4) || !aligned(prefix_len, 4)) return SAGE_ERR_ALIGNMENT;
+    a->prefix_table = prefix_table;
+    a->prefix_len = prefix_len;
+    a->max_prefix_pages = max_prefix_pages;
+    return SAGE_OK;
+}
+
+bool page_ok(int page_size) { return page_size == 16 || page_size == 32 || page_size == 64 || page_size == 128; }
+
+// The handle's device has to be the current one.
+sage_status on_device(sage_hadamard h) {
+    int dev = -1;
+    if (!current_device(&dev)) return SAGE_ERR_CUDA;
+    return dev == h->device ? SAGE_OK : SAGE_ERR_INVALID_ARG;
+}
+
+// Checks shared by the cache-write entry points and the AppendArgs they fill
+// (everything but the cache formats).
+sage_status append_args(sage_hadamard h, const sage_cview4& k, const sage_cview4& v, const float* k_mean,
+                        const int32_t* slot_map, uint8_t* k_cache, uint8_t* v_cache, int page_size, int num_pages,
+                        sage::AppendArgs* a) {
+    if (!h || !k_cache || !v_cache || page_size < 1 || num_pages < 1) return SAGE_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i)
+        if (k.size[i] != v.size[i]) return SAGE_ERR_INVALID_ARG;
+    const bool none = k.size[1] == 0;                    // a step without new tokens
+    if (!none && (!k.ptr || !v.ptr || !slot_map)) return SAGE_ERR_INVALID_ARG;
+    const int64_t size[4] = {k.size[0], none ? 1 : k.size[1], k.size[2], k.size[3]};
+    if (!sizes_ok(size, k.stride) || !sizes_ok(size, v.stride)) return SAGE_ERR_INVALID_ARG;
+    if (k.size[0] != 1 || k.size[3] != h->D) return SAGE_ERR_INVALID_ARG;
+    if (!page_ok(page_size)) return SAGE_ERR_UNSUPPORTED;
+    if (size[1] * size[2] * (h->D / 32) >= (int64_t(1) << 31) || (int64_t)num_pages * page_size >= (int64_t(1) << 31) ||
+        (int64_t)num_pages * size[2] * page_size * h->D >= (int64_t(1) << 40))
+        return SAGE_ERR_UNSUPPORTED;
+    if (!aligned(k.ptr, 2) || !aligned(v.ptr, 2) || !aligned(k_mean, 16) || !aligned(slot_map, 4) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return SAGE_ERR_ALIGNMENT;
+    a->k = to_view(k);
+    a->v = to_view(v);
+    a->k_mean = k_mean;
+    a->slot_map = slot_map;
+    a->k_cache = k_cache;
+    a->v_cache = v_cache;
+    a->page_size = page_size;
+    a->num_pages = num_pages;
+    return SAGE_OK;
+}
 
 }  // namespace
 
@@ -567,16 +622,162 @@ sage_status sage_attn_decode_mxfp4(sage_hadamard h, sage_cview4 q_bf16, const ui
     return launch_status(sage::launch_decode(a, static_cast<cudaStream_t>(stream)));
 }
 
+size_t sage_attn_decode_shared_workspace(int B, int T, int H, int Hk, int D) {
+    if (B < 1 || T < 1 || H < 1 || Hk < 1 || D < 1 || H % Hk != 0) return 0;
+    return sage::decode_shared_ws_bytes(B, T, H, Hk, D);
+}
+
+sage_status sage_attn_decode_shared(sage_hadamard h, sage_cview4 q_bf16, const uint8_t* k_cache,
+                                    const uint8_t* v_cache, const float* k_scale, const float* v_scale,
+                                    const int32_t* prefix_table, int max_prefix_pages,
+                                    const int32_t* prefix_len, const int32_t* page_table,
+                                    const int32_t* ctx_lens, int B, int T, int H, int Hk, int D,
+                                    int page_size, int max_pages, int num_pages, int window,
+                                    float softmax_scale, int kv_flags, sage_view4 out_bf16, void* ws,
+                                    size_t ws_bytes, void* stream) {
+    if (!k_cache || !v_cache || !k_scale || !v_scale) return SAGE_ERR_INVALID_ARG;
+    if (kv_flags & ~(SAGE_KV_PER_TENSOR_SCALES | SAGE_KV_V_TRANSPOSED)) return SAGE_ERR_INVALID_ARG;
+    sage::DecodeSharedArgs a;
+    sage_status st = decode_args(h, q_bf16, page_table, ctx_lens, B, T, H, Hk, D, page_size, max_pages,
+                                 num_pages, window, softmax_scale, out_bf16, nullptr, nullptr, ws, ws_bytes,
+                                 &a.d, true);
+    if (st == SAGE_OK)
+        st = shared_args(prefix_table, max_prefix_pages, prefix_len, B, T, H, Hk, page_size, max_pages, &a);
+    if (st != SAGE_OK) return st;
+    if ((kv_flags & SAGE_KV_V_TRANSPOSED) && page_size != 128) return SAGE_ERR_UNSUPPORTED;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+        return SAGE_ERR_ALIGNMENT;
+    a.d.k_cache = k_cache;
+    a.d.v_cache = v_cache;
+    a.d.k_scale = k_scale;
+    a.d.v_scale = v_scale;
+    a.d.kv_flags = kv_flags;
+    return launch_status(sage::launch_decode_shared(a, static_cast<cudaStream_t>(stream)));
+}
+
+sage_status sage_attn_decode_shared_mxfp4(sage_hadamard h, sage_cview4 q_bf16, const uint8_t* k_cache,
+                                          const uint8_t* v_cache, const uint8_t* k_sf, const uint8_t* v_sf,
+                                          const int32_t* prefix_table, int max_prefix_pages,
+                                          const int32_t* prefix_len, const int32_t* page_table,
+                                          const int32_t* ctx_lens, int B, int T, int H, int Hk, int D,
+                                          int page_size, int max_pages, int num_pages, int window,
+                                          float softmax_scale, sage_view4 out_bf16, void* ws,
+                                          size_t ws_bytes, void* stream) {
+    if (!k_cache || !v_cache || !k_sf || !v_sf) return SAGE_ERR_INVALID_ARG;
+    sage::DecodeSharedArgs a;
+    sage_status st = decode_args(h, q_bf16, page_table, ctx_lens, B, T, H, Hk, D, page_size, max_pages,
+                                 num_pages, window, softmax_scale, out_bf16, nullptr, nullptr, ws, ws_bytes,
+                                 &a.d, true);
+    if (st == SAGE_OK)
+        st = shared_args(prefix_table, max_prefix_pages, prefix_len, B, T, H, Hk, page_size, max_pages, &a);
+    if (st != SAGE_OK) return st;
+    if (D != 128) return SAGE_ERR_UNSUPPORTED;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_sf, 16) || !aligned(v_sf, 16))
+        return SAGE_ERR_ALIGNMENT;
+    a.d.k_cache = k_cache;
+    a.d.v_cache = v_cache;
+    a.d.k_scale = nullptr;
+    a.d.v_scale = nullptr;
+    a.d.kv_flags = 0;
+    a.d.mx = 1;
+    a.d.k_sf = k_sf;
+    a.d.v_sf = v_sf;
+    return launch_status(sage::launch_decode_shared(a, static_cast<cudaStream_t>(stream)));
+}
+
+sage_status sage_page_plan(const int32_t* cached_lens, const int32_t* new_lens, const int32_t* prefix_table,
+                           int prefix_pages, int32_t* free_list, const int32_t* free_count, int B,
+                           int max_pages, int page_size, int num_pages, int max_tokens, int32_t* page_table,
+                           int32_t* ctx_lens, int32_t* free_count_out, int32_t* token_offsets,
+                           int32_t* slot_map, void* stream) {
+    if (!cached_lens || !new_lens || !free_list || !free_count || !page_table || !ctx_lens ||
+        !free_count_out || !token_offsets)
+        return SAGE_ERR_INVALID_ARG;
+    if (B < 1 || max_pages < 1 || page_size < 1 || num_pages < 1 || max_tokens < 0 || prefix_pages < 0 ||
+        prefix_pages > max_pages || (prefix_pages > 0 && !prefix_table) || (max_tokens > 0 && !slot_map))
+        return SAGE_ERR_INVALID_ARG;
+    // the outputs that every part of the kernel writes while others read the lengths
+    if (ctx_lens == new_lens || free_count_out == new_lens || token_offsets == cached_lens ||
+        token_offsets == new_lens)
+        return SAGE_ERR_INVALID_ARG;
+    if (!page_ok(page_size) || B > sage::kPlanMaxRows) return SAGE_ERR_UNSUPPORTED;
+    if ((int64_t)max_pages * page_size >= (int64_t(1) << 31) || (int64_t)num_pages * page_size >= (int64_t(1) << 31))
+        return SAGE_ERR_UNSUPPORTED;
+    if (!aligned(cached_lens, 4) || !aligned(new_lens, 4) || !aligned(prefix_table, 4) || !aligned(free_list, 4) ||
+        !aligned(free_count, 4) || !aligned(page_table, 4) || !aligned(ctx_lens, 4) || !aligned(free_count_out, 4) ||
+        !aligned(token_offsets, 4) || !aligned(slot_map, 4))
+        return SAGE_ERR_ALIGNMENT;
+    sage::PlanArgs a;
+    a.cached_lens = cached_lens;
+    a.new_lens = new_lens;
+    a.prefix_table = prefix_table;
+    a.free_list = free_list;
+    a.free_count = free_count;
+    a.page_table = page_table;
+    a.ctx_lens = ctx_lens;
+    a.free_count_out = free_count_out;
+    a.token_offsets = token_offsets;
+    a.slot_map = slot_map;
+    a.B = B;
+    a.max_pages = max_pages;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.max_tokens = max_tokens;
+    a.prefix_pages = prefix_pages;
+    return launch_status(sage::launch_page_plan(a, static_cast<cudaStream_t>(stream)));
+}
+
+sage_status sage_kv_append(sage_hadamard h, sage_cview4 k_bf16, sage_cview4 v_bf16, const float* k_mean,
+                           const int32_t* slot_map, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
+                           float* v_scale, int page_size, int num_pages, int kv_flags, void* stream) {
+    if (!k_scale || !v_scale) return SAGE_ERR_INVALID_ARG;
+    if (kv_flags & ~(SAGE_KV_PER_TENSOR_SCALES | SAGE_KV_V_TRANSPOSED)) return SAGE_ERR_INVALID_ARG;
+    sage::AppendArgs a;
+    sage_status st = append_args(h, k_bf16, v_bf16, k_mean, slot_map, k_cache, v_cache, page_size, num_pages, &a);
+    if (st != SAGE_OK) return st;
+    if ((kv_flags & SAGE_KV_V_TRANSPOSED) && page_size != 128) return SAGE_ERR_UNSUPPORTED;
+    if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return SAGE_ERR_ALIGNMENT;
+    st = on_device(h);
+    if (st != SAGE_OK || a.k.size[1] == 0) return st;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.kv_flags = kv_flags;
+    return launch_status(sage::launch_kv_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+sage_status sage_kv_append_mxfp4(sage_hadamard h, sage_cview4 k_bf16, sage_cview4 v_bf16,
+                                 const float* k_mean, const int32_t* slot_map, uint8_t* k_cache,
+                                 uint8_t* v_cache, uint8_t* k_sf, uint8_t* v_sf, int page_size,
+                                 int num_pages, void* stream) {
+    if (!k_sf || !v_sf) return SAGE_ERR_INVALID_ARG;
+    sage::AppendArgs a;
+    sage_status st = append_args(h, k_bf16, v_bf16, k_mean, slot_map, k_cache, v_cache, page_size, num_pages, &a);
+    if (st != SAGE_OK) return st;
+    if (a.k.size[3] != 128) return SAGE_ERR_UNSUPPORTED;
+    if (!aligned(k_sf, 16) || !aligned(v_sf, 16)) return SAGE_ERR_ALIGNMENT;
+    st = on_device(h);
+    if (st != SAGE_OK || a.k.size[1] == 0) return st;
+    a.k_scale = nullptr;
+    a.v_scale = nullptr;
+    a.k_sf = k_sf;
+    a.v_sf = v_sf;
+    a.kv_flags = 0;
+    a.mx = 1;
+    return launch_status(sage::launch_kv_append(a, static_cast<cudaStream_t>(stream)));
+}
+
 sage_status sage_device_error_where(void* stream, int* kernel, int* site) {
     if (kernel) *kernel = 0;
     if (site) *site = 0;
     const cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-    // error words of the kernels, in the order of SAGE_KERNEL_* ids 1, 2, 3, 4
-    const unsigned words[4] = {sage::read_clear_attn_error(), sage::read_clear_decode_error(),
-                               sage::read_clear_probe_error(), sage::read_clear_attn_mx_error()};
+    // error words of the kernels, in the order of the SAGE_KERNEL_* ids 1, 2, ...
+    const unsigned words[] = {sage::read_clear_attn_error(),    sage::read_clear_decode_error(),
+                              sage::read_clear_probe_error(),   sage::read_clear_attn_mx_error(),
+                              sage::read_clear_plan_error(),    sage::read_clear_append_error()};
+    constexpr int kWords = sizeof(words) / sizeof(words[0]);
     if (e != cudaSuccess) return SAGE_ERR_CUDA;
     sage_status st = SAGE_OK;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kWords; ++i) {
         const unsigned code = words[i] & 0xFFu;
         sage_status si = SAGE_OK;
         if (code == sage::kErrTimeoutCode) si = SAGE_ERR_TIMEOUT;

@@ -146,6 +146,52 @@ struct DecodeArgs {
 size_t decode_ws_bytes(int B, int T, int H, int Hk, int D, int window);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 unsigned read_clear_decode_error();
+unsigned read_clear_decode_error();
+// a batch whose sequences begin with the same *prefix_len tokens
+struct DecodeSharedArgs {
+    DecodeArgs d;
+    const int32_t* prefix_table;            // [max_prefix_pages] physical pages
+    const int32_t* prefix_len;              // one int32
+    int max_prefix_pages;
+};
+size_t decode_shared_ws_bytes(int B, int T, int H, int Hk, int D);
+cudaError_t launch_decode_shared(const DecodeSharedArgs& a, cudaStream_t s);
+
+// ---- page planning (plan.cu)
+constexpr int kPlanMaxRows = 8192;          // requests of one plan
+struct PlanArgs {
+    const int32_t* cached_lens;             // [B]
+    const int32_t* new_lens;                // [B], < 0: the request has ended
+    const int32_t* prefix_table;            // [prefix_pages] or null
+    int32_t* free_list;                     // [num_pages], a stack of *free_count pages
+    const int32_t* free_count;
+    int32_t* page_table;                    // [B, max_pages]
+    int32_t* ctx_lens;                      // [B]
+    int32_t* free_count_out;
+    int32_t* token_offsets;                 // [B + 1]
+    int32_t* slot_map;                      // [max_tokens]
+    int B, max_pages, page_size, num_pages, max_tokens, prefix_pages;
+};
+cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t s);
+unsigned read_clear_plan_error();
+
+// ---- quantised cache write (append.cu)
+struct AppendArgs {
+    View4 k, v;                             // [1, N, Hk, D] bf16
+    const float* k_mean;                    // [Hk, D] or null
+    const int32_t* slot_map;                // [N]
+    uint8_t* k_cache;
+    uint8_t* v_cache;
+    float* k_scale;                         // per token written, per tensor read
+    float* v_scale;
+    uint8_t* k_sf = nullptr;                // MXFP4: e8m0 block scales
+    uint8_t* v_sf = nullptr;
+    int page_size, num_pages;
+    int kv_flags;                           // SAGE_KV_PER_TENSOR_SCALES | SAGE_KV_V_TRANSPOSED
+    int mx = 0;
+};
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s);
+unsigned read_clear_append_error();
 
 // ---- bounded-wait timeout probe (probe.cu)
 cudaError_t launch_wait_probe(unsigned long long limit_ns, cudaStream_t s);
