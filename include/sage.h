@@ -508,6 +508,7 @@ sage_status sage_device_error(void* stream);
 #define SAGE_KERNEL_ATTN_MX 4
 #define SAGE_KERNEL_PLAN 5
 #define SAGE_KERNEL_APPEND 6
+#define SAGE_KERNEL_SHARED 7
 
 /* sage_device_error, also saying where the reported error was recorded:
  * *kernel receives a SAGE_KERNEL_* id (0 with SAGE_OK), *site the number of

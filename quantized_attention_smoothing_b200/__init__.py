@@ -43,6 +43,7 @@ SAGE_KERNEL_PROBE = 3
 SAGE_KERNEL_ATTN_MX = 4
 SAGE_KERNEL_PLAN = 5
 SAGE_KERNEL_APPEND = 6
+SAGE_KERNEL_SHARED = 7
 SAGE_KV_PER_TENSOR_SCALES = 1
 SAGE_KV_V_TRANSPOSED = 2
 
@@ -151,25 +152,29 @@ def _check(status, where):
         raise SageError(status, where)
 
 
+# Marshalling is on the path of every call (a serving step makes several, each
+# a few microseconds of GPU time), so pointers go as plain integers (ctypes
+# converts them by the declared argument types), a view is one constructor
+# call and the current stream is read without building a stream object.
+
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _view(t, cls):
     if t.dim() != 4:
         raise ValueError("expected a 4-d tensor view, got shape %s" % (tuple(t.shape),))
-    v = cls()
-    v.ptr = t.data_ptr()
-    for i in range(4):
-        v.size[i] = t.shape[i]
-        v.stride[i] = t.stride(i)
-    return v
+    return cls(t.data_ptr(), tuple(t.shape), t.stride())
 
 
 class Hadamard:
@@ -229,7 +234,7 @@ def sage_quant_qk(h, q, k, blk_q, blk_k, q8, q_scale, k8, k_scale, k_mean=None, 
                   stream=None):
     _check(lib().sage_quant_qk(h.handle, _view(q, CView4), _view(k, CView4), int(blk_q),
                                int(blk_k), _ptr(q8), _ptr(q_scale), _ptr(k8), _ptr(k_scale),
-                               _ptr(k_mean), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                               _ptr(k_mean), _ptr(ws), _bytes(ws),
                                _stream(stream)), "sage_quant_qk")
 
 
@@ -246,7 +251,7 @@ def sage_quant_qk_noalloc(h, q, k, blk_q, blk_k, q8, q_scale, k8, k_scale, k_mea
 
 def sage_quant_k(h, k, blk_k, k8, k_scale, k_mean=None, ws=None, stream=None):
     _check(lib().sage_quant_k(h.handle, _view(k, CView4), int(blk_k), _ptr(k8), _ptr(k_scale),
-                              _ptr(k_mean), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                              _ptr(k_mean), _ptr(ws), _bytes(ws),
                               _stream(stream)), "sage_quant_k")
 
 
@@ -255,7 +260,7 @@ def sage_attn_fwd_q16(h, q, blk_q, k8, k_scale, v8_t, v_scale, Hk, Lk, blk_k, so
     _check(lib().sage_attn_fwd_q16(h.handle, _view(q, CView4), int(blk_q), _ptr(k8), _ptr(k_scale),
                                    _ptr(v8_t), _ptr(v_scale), int(Hk), int(Lk), int(blk_k),
                                    float(softmax_scale), 1 if causal else 0, _view(out, View4),
-                                   _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                                   _ptr(ws), _bytes(ws),
                                    _stream(stream)), "sage_attn_fwd_q16")
 
 
@@ -268,13 +273,13 @@ def sage_quant_qkv(h, q, k, v, blk_q, blk_k, q8, q_scale, k8, k_scale, v8_t, v_s
     _check(lib().sage_quant_qkv(h.handle, _view(q, CView4), _view(k, CView4), _view(v, CView4),
                                 int(blk_q), int(blk_k), _ptr(q8), _ptr(q_scale), _ptr(k8),
                                 _ptr(k_scale), _ptr(k_mean), _ptr(v8_t), _ptr(v_scale), _ptr(ws),
-                                0 if ws is None else ws.numel() * ws.element_size(),
+                                _bytes(ws),
                                 _stream(stream)), "sage_quant_qkv")
 
 
 def sage_quant_v(v, v8_t, v_scale, ws=None, stream=None):
     _check(lib().sage_quant_v(_view(v, CView4), _ptr(v8_t), _ptr(v_scale), _ptr(ws),
-                              0 if ws is None else ws.numel() * ws.element_size(),
+                              _bytes(ws),
                               _stream(stream)), "sage_quant_v")
 
 
@@ -283,7 +288,7 @@ def sage_attn_fwd(q8, q_scale, k8, k_scale, v8_t, v_scale, B, H, Hk, Lq, Lk, D, 
     _check(lib().sage_attn_fwd(_ptr(q8), _ptr(q_scale), _ptr(k8), _ptr(k_scale), _ptr(v8_t),
                                _ptr(v_scale), B, H, Hk, Lq, Lk, D, blk_q, blk_k,
                                float(softmax_scale), int(bool(causal)), _view(out, View4),
-                               _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(),
+                               _ptr(ws), _bytes(ws),
                                _stream(stream)), "sage_attn_fwd")
 
 
@@ -304,7 +309,7 @@ def sage_attn_decode(h, q, k_cache, v_cache, k_scale, v_scale, page_table, ctx_l
                                   B, T, H, Hk, D, int(page_size), int(max_pages), int(num_pages),
                                   int(window), float(softmax_scale), int(kv_flags), _view(out, View4),
                                   _ptr(q8_out), _ptr(q_scale_out), _ptr(ws),
-                                  0 if ws is None else ws.numel() * ws.element_size(),
+                                  _bytes(ws),
                                   _stream(stream)), "sage_attn_decode")
 
 
@@ -326,7 +331,7 @@ def sage_attn_decode_mxfp4(h, q, k_cache, v_cache, k_sf, v_sf, page_table, ctx_l
                                         B, T, H, Hk, D, int(page_size), int(max_pages), int(num_pages),
                                         int(window), float(softmax_scale), _view(out, View4),
                                         _ptr(q8_out), _ptr(q_scale_out), _ptr(ws),
-                                        0 if ws is None else ws.numel() * ws.element_size(),
+                                        _bytes(ws),
                                         _stream(stream)), "sage_attn_decode_mxfp4")
 
 
@@ -358,7 +363,7 @@ def sage_attn_decode_shared(h, q, k_cache, v_cache, k_scale, v_scale, prefix_tab
                                          _ptr(ctx_lens), B, T, H, Hk, D, int(page_size),
                                          int(page_table.shape[1]), int(num_pages), int(window),
                                          float(softmax_scale), int(kv_flags), _view(out, View4), _ptr(ws),
-                                         ws.numel() * ws.element_size(), _stream(stream)),
+                                         _bytes(ws), _stream(stream)),
            "sage_attn_decode_shared")
 
 
@@ -376,7 +381,7 @@ def sage_attn_decode_shared_mxfp4(h, q, k_cache, v_cache, k_sf, v_sf, prefix_tab
                                                _ptr(ctx_lens), B, T, H, Hk, D, int(page_size),
                                                int(page_table.shape[1]), int(num_pages), int(window),
                                                float(softmax_scale), _view(out, View4), _ptr(ws),
-                                               ws.numel() * ws.element_size(), _stream(stream)),
+                                               _bytes(ws), _stream(stream)),
            "sage_attn_decode_shared_mxfp4")
 
 
@@ -398,7 +403,7 @@ def _tokens_view(t):
     """[N, Hk, D] as the [1, N, Hk, D] view of the C ABI."""
     if t.dim() != 3:
         raise ValueError("expected [tokens, heads, head size], got shape %s" % (tuple(t.shape),))
-    return _view(t.unsqueeze(0), CView4)
+    return CView4(t.data_ptr(), (1,) + tuple(t.shape), (0,) + t.stride())
 
 
 def sage_kv_append(h, k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_mean=None, kv_flags=0,
@@ -422,7 +427,7 @@ def sage_kv_append_mxfp4(h, k, v, slot_map, k_cache, v_cache, k_sf, v_sf, k_mean
 def sage_quant_qk_mx(h, q, k, q4, q_sf, k4, k_sf, k_mean=None, ws=None, stream=None):
     _check(lib().sage_quant_qk_mx(h.handle, _view(q, CView4), _view(k, CView4), _ptr(q4), _ptr(q_sf),
                                   _ptr(k4), _ptr(k_sf), _ptr(k_mean), _ptr(ws),
-                                  0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+                                  _bytes(ws), _stream(stream)),
            "sage_quant_qk_mx")
 
 
@@ -431,7 +436,7 @@ def sage_attn_fwd_mx(q4, q_sf, k4, k_sf, v8_t, v_scale, B, H, Hk, Lq, Lk, D, sof
     _check(lib().sage_attn_fwd_mx(_ptr(q4), _ptr(q_sf), _ptr(k4), _ptr(k_sf), _ptr(v8_t), _ptr(v_scale),
                                   B, H, Hk, Lq, Lk, D, float(softmax_scale), int(bool(causal)),
                                   _view(out, View4), _ptr(ws),
-                                  0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)),
+                                  _bytes(ws), _stream(stream)),
            "sage_attn_fwd_mx")
 
 

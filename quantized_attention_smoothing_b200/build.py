@@ -27,6 +27,7 @@ SOURCES = {
     "attn_fwd.cu": [],
     "attn_mx.cu": [],
     "decode.cu": [],
+    "shared.cu": [],
     "plan.cu": [],
     "append.cu": ["-fmad=false"],
     "sage_api.cu": [],

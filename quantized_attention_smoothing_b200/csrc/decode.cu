@@ -61,16 +61,18 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "decode_common.cuh"
 #include "sage_internal.h"
 #include "sage_ptx.cuh"
 
 namespace sage {
 namespace {
 
+using namespace dec;
+
 __device__ unsigned g_decode_err;
 constexpr unsigned kErrDecodeRange = kErrRangeCode;   // ctx or page id out of range (clamped / masked)
 
-constexpr int kKeys = 128;                   // keys per tile
 constexpr int kRows = 64;                    // query rows per CTA (M of every MMA)
 constexpr int kStages = 3;                   // K / V ring
 constexpr int kScStages = 8;                 // per-token scale ring (freed by the softmax alone)
@@ -98,33 +100,10 @@ template <int NREP> struct RegSplit<true, NREP> {
     static constexpr int soft = 168, conv = NREP == 2 ? 80 : 96, prod = NREP == 2 ? 96 : 80;
     static_assert(2 * 128 * soft + 128 * conv + 128 * prod <= 512 * 128, "register split");
 };
-constexpr float kLog2e = 1.4426950408889634f;
 // A scale slot: k_scale then v_scale of the tile's keys, each by key parity
 // (index (key & 1) * kScPar + key / 2); the 4-float pad puts the two parities'
 // 16-byte reads in different banks
 constexpr int kScPar = kKeys / 2 + 4, kScHalf = 2 * kScPar, kScSlot = 2 * kScHalf;
-
-// Head size D (64 or 128): an e4m3 row of Q, K or V is D bytes, stored
-// with the swizzle of that span (128B or 64B); a bf16 V row is 2 D bytes,
-// one or two 64-channel 128B-swizzled atoms.
-// The 16-byte chunk c of row r of a D-byte swizzled e4m3 row tile.
-template <int D>
-__device__ __forceinline__ int e4m3_chunk(int c, int r) {
-    return D == 128 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
-}
-
-// Non-blocking test of the phase with the given parity.
-__device__ __forceinline__ bool mbar_test_wait(uint32_t addr, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 
 // 16 registers from 16 TMEM lanes (shape 16x64b, x16): the mapping of
 // tmem_ld16x64 over 32 columns. Valid after tmem_wait_ld16(r).
@@ -155,8 +134,6 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t (&r)[16]
     tmem_ld16x16(taddr, r);
     tmem_wait_ld16(r);
 }
-
-constexpr int al1024(int x) { return (x + 1023) & ~1023; }
 
 // N registers of 16 TMEM lanes and 2 N columns (shape 16x64b), loaded and
 // waited for: N = 64, 32 or 16.
@@ -237,6 +214,7 @@ struct DecParams {
     int cap_prefix;                          // tokens the prefix table has room for
     int pre;                                 // 1: rows of all sequences against the prefix, 0: own keys
     int cap_rows;                            // pre: tokens a sequence's table has room for
+    int late_wait;                           // nothing here depends on the preceding kernel: wait for it last
     int n_rows, n_rt;                        // pre: B T G rows of a kv head, 64-row tiles of them
     float2* ws_stat;                         // nsplit > 1: partial (m, l) [B Hk][nsplit][64]
     float* ws_o;                             //   and partial O [B Hk][nsplit][64][128] fp32
@@ -249,83 +227,6 @@ struct DecParams {
 // order.
 __device__ __forceinline__ int pv_position(int key) {
     return (key & ~15) + 8 * (key & 1) + ((key & 15) >> 1);
-}
-
-// e4m3 codes -> bf16 with exactly the same values, integer operations only.
-// A code's 7 magnitude bits placed at bf16 bits 4..10 and its sign at bit 15
-// read as a bf16 of value x * 2^-120 (exponent field e of a normal code kept,
-// a subnormal code a bf16 subnormal), and the bf16 product by 2^120 is exact.
-// `sel` picks the two code bytes of `w` (0x1404: bytes 0, 1; 0x3424: 2, 3).
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t w, uint32_t sel) {
-    const uint32_t t = __byte_perm(w, 0u, sel);          // code bytes at bits 8..15 and 24..31
-    const uint32_t bits = ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u);
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(bits), "r"(0x7B807B80u));   // 2^120
-    return r;
-}
-
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// The e4m3 codes byte m of `a` and byte m of `b` as one bf16 pair (low half
-// from `a`), exactly, as in e4m3x2_to_bf16x2; m = 0..3.
-template <int m>
-__device__ __forceinline__ uint32_t e4m3_pick_to_bf16x2(uint32_t a, uint32_t b) {
-    const uint32_t t = __byte_perm(a, b, (m << 4) | ((4 + m) << 12));   // bytes 1 and 3; 0, 2 unused
-    return bf16x2_mul(((t >> 4) & 0x07F007F0u) | (t & 0x80008000u), 0x7B807B80u);
-}
-
-// Eight E2M1 codes (OCP MX: sign, two exponent bits, one mantissa bit),
-// nibble i of `w` (bits 4i .. 4i + 3) holding element i, as four bf16 pairs:
-// pair m = (element m, element m + 4), each times the bf16 pair `c2`.
-// A code's three magnitude bits placed at bf16 bits 6..8 and its sign at bit
-// 15 read as a bf16 of value x * 2^-126 (exponent field = the code's, a
-// zero-exponent code a bf16 subnormal), so c2 = 2^(E - 1) gives x * 2^(E -
-// 127) in one exact product while that is a bf16 value.
-__device__ __forceinline__ void e2m1x8_to_bf16(uint32_t w, uint32_t c2, uint32_t* o) {
-    const uint32_t a0 = w << 6, a1 = w << 2, a2 = w >> 2, a3 = w >> 6;
-    const uint32_t s0 = w << 12, s1 = w << 8, s2 = w << 4, s3 = w;
-    o[0] = bf16x2_mul((a0 & 0x01C001C0u) | (s0 & 0x80008000u), c2);
-    o[1] = bf16x2_mul((a1 & 0x01C001C0u) | (s1 & 0x80008000u), c2);
-    o[2] = bf16x2_mul((a2 & 0x01C001C0u) | (s2 & 0x80008000u), c2);
-    o[3] = bf16x2_mul((a3 & 0x01C001C0u) | (s3 & 0x80008000u), c2);
-}
-
-// One MX block (32 E2M1 codes, 16 bytes: elements 8g .. 8g + 7 in word g)
-// times 2^(E - 127), E its e8m0 scale code, as 16 bf16 pairs: pair 4g + m =
-// (element 8g + m, element 8g + m + 4). E is read as min(E, 252), the largest
-// exponent whose values (up to 6 * 2^125) are finite in bf16, so that cache
-// bytes the window masks (slots past ctx) cannot turn a zero weight into a
-// NaN; a larger E (and E = 255, NaN) lies outside the contract.
-__device__ __forceinline__ void e2m1_block_to_bf16(uint4 u, uint32_t E, uint32_t (&o)[16]) {
-    E = min(E, 252u);
-    const uint32_t lo = E <= 128u ? E + 126u : 253u;                  // 2^(E - 1), or 2^126 then 2^(E - 127)
-    const uint32_t c2 = (lo << 7) | (lo << 23);
-    e2m1x8_to_bf16(u.x, c2, o);
-    e2m1x8_to_bf16(u.y, c2, o + 4);
-    e2m1x8_to_bf16(u.z, c2, o + 8);
-    e2m1x8_to_bf16(u.w, c2, o + 12);
-    if (E > 128u) {
-        const uint32_t c3 = (E << 7) | (E << 23);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) o[k] = bf16x2_mul(o[k], c3);
-    }
-}
-
-__device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
-
-// Barrier `id` (1..15) of `count` threads (whole warps).
-__device__ __forceinline__ void named_sync(int id, int count) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-
-// CTA-wide barrier in its non-aligned form: the threads may reach it from
-// different code (each thread arrives exactly once).
-__device__ __forceinline__ void bar_sync_all(int count) {
-    asm volatile("bar.sync 0, %0;" ::"r"(count) : "memory");
 }
 
 // Output row rr of (b, hk), channels d4 .. d4 + 3: o * inv as bf16 through
@@ -424,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    pdl_wait();
+    if (!(SHARED && p.late_wait)) pdl_wait();
     pdl_launch_dependents();
 
     int L = 0;                                       // SHARED: the prefix's length
@@ -446,8 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lo = pre ? 0 : max(SHARED ? L : 0, ctx - p.T - p.window + 1);
     const int t0 = lo / kKeys, t1 = SHARED && lo >= ctx ? t0 : (ctx + kKeys - 1) / kKeys;
     const int n_all = max(0, t1 - t0);
-    const int tb = t0 + (split * n_all) / p.nsplit;
-    const int nt = t0 + ((split + 1) * n_all) / p.nsplit - tb;
+    // SHARED: no split gets fewer than kMinTiles tiles while another has any
+    const int nsp = SHARED ? shared_splits(n_all, p.nsplit) : p.nsplit;
+    const int sp = SHARED ? min(split, nsp) : split, sp1 = SHARED ? min(split + 1, nsp) : split + 1;
+    const int tb = t0 + (sp * n_all) / nsp;
+    const int nt = t0 + (sp1 * n_all) / nsp - tb;
 
     // the producer's first page-table entries, requested before the barrier
     const int ppt = kKeys / p.page;                  // pages per tile (divides 32)
@@ -1063,13 +967,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     store_out4(p, b, hk, rr, d4, row_o4(rr, d4, st.x), st.y > 0.0f ? 1.0f / st.y : 0.0f);
                 }
             } else {
-                // the partial to the workspace, combined by decode_merge_kernel
+                // the partial to the workspace, combined by a merge kernel
                 const size_t part = (size_t)bhk * p.nsplit + split;
-                float4* wo = reinterpret_cast<float4*>(p.ws_o + part * kRows * kD);
-                // (SHARED: a part with no key leaves its statistics alone)
-                for (int idx = tid; idx < (SHARED && nt == 0 ? 0 : R * (kD / 4)); idx += kSoftWarps * 32) {
-                    const int rr = idx / (kD / 4), d4 = 4 * (idx % (kD / 4));
-                    wo[idx] = row_o4(rr, d4, row_stat(rr).x);
+                if constexpr (SHARED) {
+                    // channel-major [D][64 rows], as the merge over the parts
+                    // reads it; a part with no key leaves its statistics alone
+                    float* wo = p.ws_o + part * kRows * kD;
+                    const int work = nt == 0 ? 0 : R * (kD / 4);
+                    for (int idx = tid; idx < work; idx += kSoftWarps * 32) {
+                        const int rr = idx % R, d4 = 4 * (idx / R);
+                        const float4 o = row_o4(rr, d4, row_stat(rr).x);
+                        wo[d4 * kRows + rr] = o.x;
+                        wo[(d4 + 1) * kRows + rr] = o.y;
+                        wo[(d4 + 2) * kRows + rr] = o.z;
+                        wo[(d4 + 3) * kRows + rr] = o.w;
+                    }
+                } else {
+                    float4* wo = reinterpret_cast<float4*>(p.ws_o + part * kRows * kD);
+                    for (int idx = tid; idx < R * (kD / 4); idx += kSoftWarps * 32) {
+                        const int rr = idx / (kD / 4), d4 = 4 * (idx % (kD / 4));
+                        wo[idx] = row_o4(rr, d4, row_stat(rr).x);
+                    }
                 }
                 if (tid < R) p.ws_stat[part * kRows + tid] = row_stat(tid);
             }
@@ -1197,6 +1115,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         bar_sync_all(kThreads);
     }
+    if (SHARED && p.late_wait) pdl_wait();       // this grid ends after the one before it
 }
 
 // The splits of (b, hk) combined (log-sum-exp): thread = one query row and
@@ -1240,84 +1159,11 @@ __global__ void __launch_bounds__(256) decode_merge_kernel(const DecParams p) {
     store_out4(p, b, hk, rr, d4, acc, den > 0.0f ? 1.0f / den : 0.0f);
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// The cache [num_pages, Hk, page, D] e4m3 as a 3-D map {D bytes, page
-// rows, num_pages * Hk}; one box = one page of one kv head, with the swizzle
-// of a D-byte row (128B or 64B).
-bool encode_cache(CUtensorMap* map, const void* ptr, int num_pages, int Hk, int page, int D) {
-    auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
-    if (!enc) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page),
-                                static_cast<cuuint64_t>(num_pages) * Hk};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page) * D};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(page), 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The transposed V cache [num_pages, Hk, D, page = 128] as a 3-D map
-// {128 key bytes, D channel rows, num_pages * Hk}; one box = one page of
-// one kv head as [channel][key], 128B swizzle.
-bool encode_cache_vt(CUtensorMap* map, const void* ptr, int num_pages, int Hk, int D) {
-    auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
-    if (!enc) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kKeys), static_cast<cuuint64_t>(D),
-                                static_cast<cuuint64_t>(num_pages) * Hk};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kKeys), static_cast<cuuint64_t>(D) * kKeys};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kKeys), static_cast<cuuint32_t>(D), 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// The MXFP4 cache codes [num_pages, Hk, page, D / 2] bytes (two E2M1 codes a
-// byte) as a 3-D map {D / 2 bytes, page rows, num_pages * Hk}; one box = one
-// page of one kv head, 64B swizzle (D = 128: 64-byte rows).
-bool encode_cache_mx(CUtensorMap* map, const void* ptr, int num_pages, int Hk, int page, int D) {
-    auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
-    if (!enc || D != 128) return false;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D / 2), static_cast<cuuint64_t>(page),
-                                static_cast<cuuint64_t>(num_pages) * Hk};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D / 2), static_cast<cuuint64_t>(page) * (D / 2)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(D / 2), static_cast<cuuint32_t>(page), 1};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool MX>
 constexpr int smem_bytes() { return SmL<D, MX>::kBytes + 1024; }
 
 // Repeats of the query rows in the QK A operand for R query rows.
 int pick_nrep(int R) { return R <= 16 ? 4 : (R <= 32 ? 2 : 1); }
-
-// Streaming multiprocessors of the current device (queried once per device).
-int device_sms() {
-    static std::mutex mu;
-    static int cache[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 1;
-    std::lock_guard<std::mutex> lock(mu);
-    int& c = cache[dev];
-    if (c == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
-            cudaGetLastError();
-            n = 1;
-        }
-        c = n;
-    }
-    return c;
-}
 
 // The most CTAs per (sequence, kv head): a split grid stays within one wave
 // (one CTA per SM), so that it and the merge are all the work there is.
@@ -1449,122 +1295,52 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// ---- a batch that shares a prefix
-
-// Where the partials of the two passes lie in the workspace.
-struct SharedPlan {
-    int n_rt, np, ns;                        // 64-row tiles of a kv head, their splits, a sequence's splits
-    size_t pre_stat, pre_o, own_stat, own_o, bytes;
-};
-
-SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
-    SharedPlan w;
-    const int64_t rows = (int64_t)B * T * (H / Hk);
-    w.n_rt = (int)ceil_div(rows, kRows);
-    w.np = (int)std::max<int64_t>(1, std::min<int64_t>(64, device_sms() / ((int64_t)w.n_rt * Hk)));
-    w.ns = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxSplit, device_sms() / ((int64_t)B * Hk)));
-    const size_t pre = (size_t)w.n_rt * Hk * w.np * kRows, own = (size_t)B * Hk * w.ns * kRows;
-    w.pre_stat = 0;
-    w.own_stat = w.pre_stat + pre * sizeof(float2);
-    w.pre_o = w.own_stat + own * sizeof(float2);
-    w.own_o = w.pre_o + pre * D * sizeof(float);
-    w.bytes = w.own_o + own * D * sizeof(float);
-    return w;
-}
-
-// The prefix's and the sequence's own parts of every query row combined
-// (log-sum-exp): thread = one row and four channels.
-template <int D>
-__global__ void __launch_bounds__(128) shared_merge_kernel(const DecParams p, const float2* __restrict__ pre_stat,
-                                                           const float* __restrict__ pre_o, int np,
-                                                           const float2* __restrict__ own_stat,
-                                                           const float* __restrict__ own_o, int ns) {
-    const int idx = blockIdx.x * 128 + threadIdx.x, hk = blockIdx.y;
-    const int n = idx / (D / 4), d4 = 4 * (idx % (D / 4));
-    if (n >= p.n_rows) return;
-    const int b = n / p.R, rr = n % p.R;
-    const size_t part_p = ((size_t)hk * p.n_rt + n / kRows) * np, part_o = ((size_t)b * p.Hk + hk) * ns;
-    float M = -INFINITY, den = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto take = [&](const float2* st, const float* o, size_t part, int count, int r) {
-        for (int sp = 0; sp < count; ++sp) {
-            const float2 s = __ldcg(st + (part + sp) * kRows + r);
-            if (s.x == -INFINITY) continue;
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(o + ((part + sp) * kRows + r) * D + d4));
-            const float m = fmaxf(M, s.x);
-            const float wa = M == -INFINITY ? 0.0f : ex2_approx(M - m), wb = ex2_approx(s.x - m);
-            den = fmaf(den, wa, wb * s.y);
-            acc.x = fmaf(acc.x, wa, wb * v.x);
-            acc.y = fmaf(acc.y, wa, wb * v.y);
-            acc.z = fmaf(acc.z, wa, wb * v.z);
-            acc.w = fmaf(acc.w, wa, wb * v.w);
-            M = m;
-        }
-    };
-    take(pre_stat, pre_o, part_p, np, n % kRows);
-    take(own_stat, own_o, part_o, ns, rr);
-    store_out4(p, b, hk, rr, d4, acc, den > 0.0f ? 1.0f / den : 0.0f);
-}
-
 template <int D, bool MX>
-cudaError_t launch_decode_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
+cudaError_t launch_part_d(const DecodeArgs& a, const SharedPart& sp, cudaStream_t s) {
     constexpr int kSmemBytes = smem_bytes<D, MX>();
-    const DecodeArgs& a = sa.d;
     DecParams p;
     CUtensorMap tk, tv;
     cudaError_t e = decode_setup<D, MX>(a, p, tk, tv);
     if (e != cudaSuccess) return e;
-    const SharedPlan w = shared_plan(a.B, a.T, a.H, a.Hk, D);
-    uint8_t* ws = static_cast<uint8_t*>(a.ws);
-    p.plen = sa.prefix_len;
-    p.cap_prefix = sa.max_prefix_pages * a.page_size;
+    p.plen = sp.prefix_len;
+    p.cap_prefix = sp.max_prefix_pages * a.page_size;
     p.cap_rows = a.max_pages * a.page_size;
     p.n_rows = a.B * p.R;
-    p.n_rt = w.n_rt;
-    auto pass = [&](const DecParams& q, int rows, dim3 grid) -> cudaError_t {
-        const int nrep = pick_nrep(rows);
-        auto kern = nrep == 4 ? decode_kernel<D, MX, 4, true>
-                              : (nrep == 2 ? decode_kernel<D, MX, 2, true> : decode_kernel<D, MX, 1, true>);
-        cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-        return r != cudaSuccess ? r : launch_pdl(kern, grid, dim3(kThreads), kSmemBytes, s, tk, tv, q);
-    };
-    DecParams q = p;
-    q.pre = 1;
-    q.ptab = sa.prefix_table;
-    q.max_pages = sa.max_prefix_pages;
-    q.nsplit = w.np;
-    q.ws_stat = reinterpret_cast<float2*>(ws + w.pre_stat);
-    q.ws_o = reinterpret_cast<float*>(ws + w.pre_o);
-    e = pass(q, std::min(p.n_rows, kRows), dim3(w.np, w.n_rt * a.Hk));
+    p.n_rt = sp.n_rt;
+    p.nsplit = sp.nsplit;
+    p.ws_stat = sp.stat;
+    p.ws_o = sp.o;
+    p.pre = sp.pre;
+    p.late_wait = sp.late_wait;
+    if (sp.pre) {
+        p.ptab = sp.prefix_table;
+        p.max_pages = sp.max_prefix_pages;
+    }
+    const int nrep = pick_nrep(sp.pre ? std::min(p.n_rows, kRows) : p.R);
+    auto kern = nrep == 4 ? decode_kernel<D, MX, 4, true>
+                          : (nrep == 2 ? decode_kernel<D, MX, 2, true> : decode_kernel<D, MX, 1, true>);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
-    p.nsplit = w.ns;
-    p.ws_stat = reinterpret_cast<float2*>(ws + w.own_stat);
-    p.ws_o = reinterpret_cast<float*>(ws + w.own_o);
-    e = pass(p, p.R, dim3(w.ns, a.B * a.Hk));
-    if (e != cudaSuccess) return e;
-    shared_merge_kernel<D><<<dim3((unsigned)ceil_div((int64_t)p.n_rows * (D / 4), 128), a.Hk), 128, 0, s>>>(
-        p, q.ws_stat, q.ws_o, w.np, p.ws_stat, p.ws_o, w.ns);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3(sp.nsplit, sp.pre ? sp.n_rt * a.Hk : a.B * a.Hk), dim3(kThreads), kSmemBytes, s, tk,
+                      tv, p);
 }
 
 }  // namespace
 
-size_t decode_shared_ws_bytes(int B, int T, int H, int Hk, int D) { return shared_plan(B, T, H, Hk, D).bytes; }
+cudaError_t launch_decode_part(const DecodeArgs& a, const SharedPart& p, cudaStream_t s) {
+    if (a.mx) return a.D == 128 ? launch_part_d<128, true>(a, p, s) : cudaErrorInvalidValue;
+    switch (a.D) {
+        case 64: return launch_part_d<64, false>(a, p, s);
+        case 128: return launch_part_d<128, false>(a, p, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
 
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
     if (a.mx) return a.D == 128 ? launch_decode_d<128, true>(a, s) : cudaErrorInvalidValue;
     switch (a.D) {
         case 64: return launch_decode_d<64, false>(a, s);
         case 128: return launch_decode_d<128, false>(a, s);
-        default: return cudaErrorInvalidValue;
-    }
-}
-
-cudaError_t launch_decode_shared(const DecodeSharedArgs& a, cudaStream_t s) {
-    if (a.d.mx) return a.d.D == 128 ? launch_decode_shared_d<128, true>(a, s) : cudaErrorInvalidValue;
-    switch (a.d.D) {
-        case 64: return launch_decode_shared_d<64, false>(a, s);
-        case 128: return launch_decode_shared_d<128, false>(a, s);
         default: return cudaErrorInvalidValue;
     }
 }

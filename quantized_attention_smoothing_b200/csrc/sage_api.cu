@@ -773,7 +773,8 @@ sage_status sage_device_error_where(void* stream, int* kernel, int* site) {
     // error words of the kernels, in the order of the SAGE_KERNEL_* ids 1, 2, ...
     const unsigned words[] = {sage::read_clear_attn_error(),    sage::read_clear_decode_error(),
                               sage::read_clear_probe_error(),   sage::read_clear_attn_mx_error(),
-                              sage::read_clear_plan_error(),    sage::read_clear_append_error()};
+                              sage::read_clear_plan_error(),    sage::read_clear_append_error(),
+                              sage::read_clear_shared_error()};
     constexpr int kWords = sizeof(words) / sizeof(words[0]);
     if (e != cudaSuccess) return SAGE_ERR_CUDA;
     sage_status st = SAGE_OK;
