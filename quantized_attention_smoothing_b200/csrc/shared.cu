@@ -120,6 +120,739 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) 
     dst[p.os3] = __float2bfloat16_rn(y1);
 }
 
+// ------------------------------------------------------------------ prefix
+
+// CTA = 16 warps:
+//   warps 0-7   softmax, two groups of four; thread = one query row (TMEM lane)
+//               and all 128 keys of a unit, so the row statistics need no
+//               shuffles;
+//   warps 8-11  V converters: e4m3 -> exact bf16 (MXFP4: K and V);
+//   warp 12     K/V producer (one TMA box per page), warp 13 MMA issuer and
+//               TMEM owner, warp 14 scale producer, warp 15 barriers.
+// A unit is one 128-row x 128-key block of S; unit u belongs to group u & 1.
+// RG = 2 (256 rows a CTA): group g holds rows 128 g .., units 2 i and 2 i + 1
+// are the two halves of key tile i, so a tile is loaded and converted once for
+// 256 rows. RG = 1 (128 rows): both groups hold the same rows, unit i is key
+// tile i, and the groups' (m, l, O) are combined at the end.
+// Per unit: S = Q8 K8^T (TMEM, fp32, M = N = 128) -> y = S k_scale -> row max
+// -> p = 2^(y c - m) -> P = bf16(p v_scale), written over S's own columns as
+// the A operand (in TMEM) of O += P V. TMEM is full with that (S 2 x 128, O 2
+// x D columns), so QK(u + 2) is issued when PV(u) has completed; the other
+// group's softmax fills the gap.
+// The running max is only raised when a row's new maximum exceeds it by more
+// than 8 (base 2): p then stays below 2^8, which fp32 sums and bf16 weights
+// hold as exactly as values below one, and most tiles leave O alone.
+constexpr int kStages = 3;                   // K / V ring
+constexpr int kScStages = 8;                 // scale ring
+constexpr int kThreads = 512;
+constexpr int kConvWarp0 = 8, kTmaWarp = 12, kMmaWarp = 13, kScaleWarp = 14, kInitWarp = 15;
+// 256 x 200 + 128 x 64 + 128 x 48 = 512 x 128 registers, the launch's own
+constexpr int kRegsSoft = 200, kRegsConv = 64, kRegsProd = 48;
+static_assert(256 * kRegsSoft + 128 * kRegsConv + 128 * kRegsProd <= kThreads * 128, "register split");
+constexpr float kLazyMax = 8.0f;
+
+struct PrefixParams {
+    const uint16_t* q;
+    int64_t qs0, qs1, qs2, qs3;
+    int q_vec;
+    const float* ksc;
+    const float* vsc;
+    int per_tensor, v_trans;
+    const uint8_t* ksf8;
+    const uint8_t* vsf8;
+    const int32_t* ptab;
+    const int32_t* plen;
+    const int32_t* ctx;
+    int T, Hk, G, R, n_rows, page, lg_page, cap_prefix, cap_rows, num_pages, window, np, n_rt;
+    float logit_scale_log2;
+    float2* stat;                            // [Hk n_rt][np][128 RG]
+    float* o;                                // [Hk n_rt][np][D][128 RG]
+};
+
+template <int D, bool MX, int RG>
+struct SmP {
+    static constexpr int kRowsCta = 128 * RG;
+    static constexpr int kQRow = MX ? 2 * D : D;                     // bytes of a query row
+    static constexpr int kKStage = MX ? kKeys * D / 2 : kKeys * D;
+    static constexpr int kSfStage = MX ? kKeys * D / 32 : 0;
+    static constexpr int kQ = 0;                                     // e4m3 [rows][D]; MX bf16 [group][2 atoms][128][128 B]
+    static constexpr int kK = kQ + kRowsCta * kQRow;
+    static constexpr int kV = kK + kStages * kKStage;
+    static constexpr int kKsf = kV + kStages * kKStage;
+    static constexpr int kVsf = kKsf + kStages * kSfStage;
+    static constexpr int kKb = MX ? al1024(kVsf + kStages * kSfStage) : kVsf;
+    static constexpr int kKbBuf = MX ? kKeys * 2 * D : 0;
+    static constexpr int kVb = kKb + kKbBuf;                         // [2] bf16 V, D / 64 atoms [128][128 B]
+    static constexpr int kVbBuf = kKeys * 2 * D;
+    static constexpr int kScale = kVb + 2 * kVbBuf;                  // [slot][k | v][128] fp32
+    static constexpr int kScSlot = MX ? 0 : 2 * kKeys;
+    static constexpr int kSq = kScale + kScStages * kScSlot * 4;     // [rows] query scales
+    static constexpr int kMeta = kSq + kRowsCta * 4;                 // [slot] bad-page mask
+    static constexpr int kSpan = kMeta + kScStages * 4;              // [8 warps] lowest, highest key any row sees
+    static constexpr int kBar = kSpan + 2 * 8 * 4;
+    static constexpr int kKvFull = 0, kKvEmpty = kKvFull + kStages, kSFull = kKvEmpty + kStages, kPReady = kSFull + 2,
+                         kPvDone = kPReady + 2, kVReady = kPvDone + 2, kVFree = kVReady + 2, kFinal = kVFree + 2,
+                         kQReady = kFinal + 1, kScFull = kQReady + 1, kScEmpty = kScFull + kScStages,
+                         kKbReady = kScEmpty + kScStages, kKbFree = kKbReady + 1, kNumBars = kKbFree + 1;
+    static constexpr int kMisc = kBar + kNumBars * 8;                // TMEM base, abort flag
+    static constexpr int kBytes = kMisc + 16;
+    // RG = 1: the other group's half of O, [D][128] fp32, over the code stages
+    static constexpr int kX = kK;
+    static constexpr int kXStat = kX + 128 * D * 4;                  // [2 groups][128] (m, l)
+    static_assert(RG == 2 || kXStat + 2 * 128 * 8 <= kVb, "exchange area");
+    static_assert(kK % 1024 == 0 && kV % 1024 == 0 && kVb % 1024 == 0 && kKb % 1024 == 0, "swizzled tiles");
+    static_assert(kBar % 8 == 0 && kKsf % 16 == 0 && kScale % 16 == 0, "alignment");
+    static_assert(kBytes + 1024 <= 227 * 1024, "shared memory");
+};
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 x bf16 -> fp32 (A: lane = row, a
+// 32-bit column two consecutive keys).
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+template <int D, bool MX, int RG>
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const PrefixParams p) {
+    using Sm = SmP<D, MX, RG>;
+    constexpr int kRowsCta = Sm::kRowsCta;
+    constexpr int kQe = D / 4;                    // query elements per rotating thread (4 per row)
+    constexpr int kLgQe = D == 128 ? 5 : 4;
+    constexpr uint32_t kOCol = 256;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Sm::kBar);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Sm::kMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Sm::kMisc + 4);
+    float* sq = reinterpret_cast<float*>(sm + Sm::kSq);
+    int* meta = reinterpret_cast<int*>(sm + Sm::kMeta);
+    int* span = reinterpret_cast<int*>(sm + Sm::kSpan);
+    float* scl = reinterpret_cast<float*>(sm + Sm::kScale);
+    const int split = blockIdx.x, hk = blockIdx.y / p.n_rt, rt = blockIdx.y % p.n_rt;
+    const int row0 = rt * kRowsCta;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (warp == kInitWarp) {
+        for (int i = lane; i < Sm::kNumBars; i += 32) {
+            uint32_t cnt = 1;                                                          // expect_tx; commits
+            if (i >= Sm::kKvEmpty && i < Sm::kKvEmpty + kStages) cnt = MX ? 4 : 1 + 4; // (QK commit +) converters
+            if (i >= Sm::kPReady && i < Sm::kPReady + 2) cnt = 4;                      // softmax group
+            if (i >= Sm::kVReady && i < Sm::kVReady + 2) cnt = 4;                      // converters
+            if (i == Sm::kQReady) cnt = 8;
+            if (i >= Sm::kScFull && i < Sm::kScFull + kScStages) cnt = 1 + 32;
+            if (i >= Sm::kScEmpty && i < Sm::kScEmpty + kScStages) cnt = 4 * RG;       // the groups that read the tile
+            if (i == Sm::kKbReady) cnt = 4;
+            mbar_init(&bars[i], cnt);
+        }
+        if (lane == 0) *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    if (warp == kTmaWarp && lane == 0) {
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+
+    int L = *p.plen;
+    if (L > p.cap_prefix || L < 0) {
+        if (tid == 0 && split == 0) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
+        L = max(0, min(L, p.cap_prefix));
+    }
+    // the softmax thread's row, and the keys of the prefix that it sees
+    const int g = (warp >> 2) & 1;
+    const int r = RG == 2 ? (tid & 255) : (tid & 127);
+    const int n = row0 + r;
+    const bool rv = n < p.n_rows;
+    int key_lo = INT32_MAX, key_hi = -1;
+    if (warp < 8 && rv) {
+        const int ctx = max(0, min(__ldg(p.ctx + n / p.R), p.cap_rows));
+        const int pq = ctx - p.T + (n % p.R) / p.G;
+        key_lo = max(0, pq - p.window + 1);
+        key_hi = min(pq, L - 1);
+        if (key_hi < key_lo) {
+            key_lo = INT32_MAX;
+            key_hi = -1;
+        }
+    }
+    if (warp < 8) {
+        const int lo = __reduce_min_sync(0xffffffffu, key_lo), hi = __reduce_max_sync(0xffffffffu, key_hi);
+        if (lane == 0) {
+            span[warp] = lo;
+            span[8 + warp] = hi;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    int lo = INT32_MAX, hi = -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        lo = min(lo, span[i]);
+        hi = max(hi, span[8 + i]);
+    }
+    // key tiles [t0, t0 + n_all) that some row of the CTA sees; this split's share
+    const int t0 = hi >= 0 ? lo / kKeys : 0;
+    const int n_all = hi >= 0 ? hi / kKeys + 1 - t0 : 0;
+    const int nsp = shared_splits(n_all, p.np);
+    const int tb = t0 + (int)((int64_t)min(split, nsp) * n_all / nsp);
+    const int nt = t0 + (int)((int64_t)min(split + 1, nsp) * n_all / nsp) - tb;
+    const int nu = RG * nt;                       // units
+    const int ppt = kKeys / p.page;
+    const size_t part = (size_t)blockIdx.y * p.np + split;
+
+    if (warp >= kTmaWarp) {
+      reg_dealloc<kRegsProd>();
+      if (warp == kTmaWarp || warp == kScaleWarp) {
+        // ------------------------------------------------------------ producers
+        // (as decode.cu's: lane j of chunk c looks up page 32 c + j of the
+        // CTA's pages; a page that holds no key below L is not looked up)
+        const bool kv = warp == kTmaWarp;
+        const float ks_t = !MX && !kv && p.per_tensor ? __ldg(p.ksc) : 1.0f;
+        const float vs_t = !MX && !kv && p.per_tensor ? __ldg(p.vsc) : 1.0f;
+        int chunk = -1, phys = 0, issued = 0;
+        bool bad = false;
+        for (int i = 0; i < nt; ++i) {
+            const int s = i % kStages, c = i % kScStages;
+            const bool free_slot =
+                kv ? mbar_wait(&bars[Sm::kKvEmpty + s], ((i / kStages) & 1) ^ 1, abort_flag, &g_shared_err, 1)
+                   : mbar_wait(&bars[Sm::kScEmpty + c], ((i / kScStages) & 1) ^ 1, abort_flag, &g_shared_err, 2);
+            if (!warp_all(free_slot)) break;
+            if ((i * ppt) / 32 != chunk) {
+                chunk = (i * ppt) / 32;
+                const int lp = tb * ppt + 32 * chunk + lane;
+                phys = 0;
+                bad = false;
+                if (lp < (tb + nt) * ppt && lp * p.page < L) {
+                    const int pg = __ldg(p.ptab + lp);
+                    if (pg < 0 || pg >= p.num_pages) {
+                        bad = true;
+                        if (kv) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
+                    } else {
+                        phys = pg;
+                    }
+                }
+            }
+            const int slot0 = (i * ppt) % 32;
+            const bool mine = lane >= slot0 && lane < slot0 + ppt;
+            if (kv) {
+                if (lane == slot0)
+                    mbar_arrive_expect_tx(&bars[Sm::kKvFull + s], 2 * (Sm::kKStage + Sm::kSfStage));
+                __syncwarp();
+                if (mine) {
+                    const int z = phys * p.Hk + hk, q = lane - slot0;
+                    constexpr int kRowB = Sm::kKStage / kKeys;
+                    tma_load_3d(sm + Sm::kK + s * Sm::kKStage + q * p.page * kRowB, &tmK, &bars[Sm::kKvFull + s], 0, 0, z);
+                    tma_load_3d(sm + Sm::kV + s * Sm::kKStage + q * p.page * kRowB, &tmV, &bars[Sm::kKvFull + s], 0, 0, z);
+                    if constexpr (MX) {
+                        constexpr int kSfB = D / 32;
+                        const int64_t off = (int64_t)z * p.page * kSfB;
+                        bulk_load(sm + Sm::kKsf + s * Sm::kSfStage + q * p.page * kSfB, p.ksf8 + off, p.page * kSfB,
+                                  &bars[Sm::kKvFull + s]);
+                        bulk_load(sm + Sm::kVsf + s * Sm::kSfStage + q * p.page * kSfB, p.vsf8 + off, p.page * kSfB,
+                                  &bars[Sm::kKvFull + s]);
+                    }
+                }
+            } else {
+                const unsigned badm = __ballot_sync(0xffffffffu, mine && bad) >> slot0;
+                if (lane == 0) {
+                    meta[c] = static_cast<int>(badm);
+                    mbar_arrive(&bars[Sm::kScFull + c]);
+                }
+                if constexpr (MX) {
+                    mbar_arrive(&bars[Sm::kScFull + c]);
+                } else {
+                    float* dst = scl + c * Sm::kScSlot + 4 * lane;       // keys 4 lane .. 4 lane + 3
+                    if (p.per_tensor) {
+                        *reinterpret_cast<float4*>(dst) = make_float4(ks_t, ks_t, ks_t, ks_t);
+                        *reinterpret_cast<float4*>(dst + kKeys) = make_float4(vs_t, vs_t, vs_t, vs_t);
+                        mbar_arrive(&bars[Sm::kScFull + c]);
+                    } else {
+                        const int pq = __shfl_sync(0xffffffffu, phys, slot0 + 4 * lane / p.page);
+                        const int64_t src = ((int64_t)pq * p.Hk + hk) * p.page + (4 * lane) % p.page;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            cp_async_4(dst + e, p.ksc + src + e);
+                            cp_async_4(dst + kKeys + e, p.vsc + src + e);
+                        }
+                        cp_async_mbar_arrive(&bars[Sm::kScFull + c]);
+                    }
+                }
+            }
+            issued = i + 1;
+        }
+        // no copy of this CTA may land after it exits
+        if (kv) {
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                mbar_wait_drain(&bars[Sm::kKvFull + i % kStages], (i / kStages) & 1);
+        } else {
+            for (int i = max(0, issued - kScStages); i < issued; ++i)
+                mbar_wait_drain(&bars[Sm::kScFull + i % kScStages], (i / kScStages) & 1);
+        }
+      } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0 && nt > 0) {
+            constexpr uint32_t kIdescQK = umma_idesc(1, MX ? 1 : 0, 128, kKeys);
+            constexpr uint32_t kIdescPV = umma_idesc(1, 1, 128, D) | (1u << 16);       // B MN-major
+            constexpr uint32_t kIdescPVT = umma_idesc(1, 1, 128, D);                   // B K-major (V^T)
+            const uint64_t qdesc = umma_desc_kmajor(smem_u32(sm + Sm::kQ), MX ? 128 : D);
+            const uint64_t vlbo = (p.v_trans || D == 64)
+                                      ? 0ull
+                                      : (static_cast<uint64_t>((kKeys * 128) >> 4) << 16) - (1ull << 16);
+            const uint64_t vdesc = umma_desc_kmajor(smem_u32(sm + Sm::kVb), 128) + vlbo;
+            auto issue_qk = [&](int u) -> bool {
+                const int gu = u & 1, i = RG == 2 ? u >> 1 : u, s = i % kStages;
+                const bool first = RG == 1 || gu == 0, last = RG == 1 || gu == 1;
+                const uint32_t dst = tmem + 128 * gu;
+                const uint64_t qd = qdesc + (RG == 2 ? gu : 0) * ((128 * Sm::kQRow) >> 4);
+                if constexpr (MX) {
+                    if (first && !mbar_wait(&bars[Sm::kKbReady], i & 1, abort_flag, &g_shared_err, 3)) return false;
+                    tc_fence_after();
+                    const uint64_t kd = umma_desc_kmajor(smem_u32(sm + Sm::kKb), 128);
+#pragma unroll
+                    for (int st = 0; st < D / 16; ++st)
+                        mma_bf16_ss(dst, qd + (st >> 2) * ((128 * 128) >> 4) + 2 * (st & 3),
+                                    kd + (st >> 2) * ((kKeys * 128) >> 4) + 2 * (st & 3), kIdescQK, st > 0 ? 1u : 0u);
+                    mma_commit(&bars[Sm::kSFull + gu]);
+                    if (last) mma_commit(&bars[Sm::kKbFree]);
+                } else {
+                    if (first && !mbar_wait(&bars[Sm::kKvFull + s], (i / kStages) & 1, abort_flag, &g_shared_err, 3))
+                        return false;
+                    tc_fence_after();
+                    const uint64_t kd = umma_desc_kmajor(smem_u32(sm + Sm::kK + s * Sm::kKStage), D);
+#pragma unroll
+                    for (int kk = 0; kk < D / 32; ++kk)
+                        mma_f8_ss(dst, qd + 2 * kk, kd + 2 * kk, kIdescQK, kk > 0 ? 1u : 0u);
+                    mma_commit(&bars[Sm::kSFull + gu]);
+                    if (last) mma_commit(&bars[Sm::kKvEmpty + s]);
+                }
+                return true;
+            };
+            bool ok = mbar_wait(&bars[Sm::kQReady], 0, abort_flag, &g_shared_err, 4);
+            if (ok) ok = issue_qk(0);
+            if (ok && nu > 1) ok = issue_qk(1);
+            for (int u = 0; ok && u < nu; ++u) {
+                const int gu = u & 1, i = RG == 2 ? u >> 1 : u, vb = i & 1;
+                if (RG == 1 || gu == 0)
+                    ok = mbar_wait(&bars[Sm::kVReady + vb], (i >> 1) & 1, abort_flag, &g_shared_err, 5);
+                if (ok) ok = mbar_wait(&bars[Sm::kPReady + gu], (u >> 1) & 1, abort_flag, &g_shared_err, 6);
+                if (!ok) break;
+                // O[gu] += P(u) V(i): 8 steps of 16 keys
+                tc_fence_after();
+                const uint64_t vd = vdesc + vb * (Sm::kVbBuf >> 4);
+                const uint32_t odst = tmem + kOCol + 128 * gu, pa = tmem + 128 * gu;
+                if (!p.v_trans) {
+#pragma unroll
+                    for (int st = 0; st < kKeys / 16; ++st)
+                        mma_bf16_ts(odst, pa + 8 * st, vd + 128 * st, kIdescPV, (u > 1 || st > 0) ? 1u : 0u);
+                } else {
+#pragma unroll
+                    for (int st = 0; st < kKeys / 16; ++st)
+                        mma_bf16_ts(odst, pa + 8 * st, vd + (st >> 2) * ((D * 128) >> 4) + 2 * (st & 3), kIdescPVT,
+                                    (u > 1 || st > 0) ? 1u : 0u);
+                }
+                mma_commit(&bars[Sm::kPvDone + gu]);
+                if (RG == 1 || gu == 1) mma_commit(&bars[Sm::kVFree + vb]);
+                // S(u + 2) takes the columns that P(u) holds
+                if (u + 2 < nu) {
+                    ok = mbar_wait(&bars[Sm::kPvDone + gu], (u >> 1) & 1, abort_flag, &g_shared_err, 7);
+                    if (ok) ok = issue_qk(u + 2);
+                }
+            }
+            mma_commit(&bars[Sm::kFinal]);
+            mbar_wait_drain(&bars[Sm::kFinal], 0);
+        }
+      }
+    } else if (warp < 8) {
+      reg_alloc<kRegsSoft>();
+        // ------------------------------------------------------------ softmax
+        // ---- query rows: rotate and quantise to e4m3, four threads per row,
+        // 64 rows a pass (the operations of decode.cu)
+        for (int pass = 0; pass < 2 * RG; ++pass) {
+            const int qr = 64 * pass + (tid >> 2), qq = tid & 3, nq = row0 + qr;
+            const bool qv = nq < p.n_rows;
+            const int bq = qv ? nq / p.R : 0, rq = qv ? nq % p.R : 0;
+            const uint16_t* src = p.q + bq * p.qs0 + (rq / p.G) * p.qs1 + (int64_t)(hk * p.G + rq % p.G) * p.qs2 +
+                                  (int64_t)(qq * kQe) * p.qs3;
+            float x[kQe];
+            if (p.q_vec) {
+#pragma unroll
+                for (int c = 0; c < kQe / 8; ++c) {
+                    const uint4 w = qv ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[8 * c + 2 * e] = __uint_as_float(wd[e] << 16);
+                        x[8 * c + 2 * e + 1] = __uint_as_float(wd[e] & 0xFFFF0000u);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int d = 0; d < kQe; ++d)
+                    x[d] = qv ? __uint_as_float(static_cast<uint32_t>(__ldg(src + d * p.qs3)) << 16) : 0.0f;
+            }
+#pragma unroll
+            for (int lg = 0; lg < kLgQe; ++lg) {
+                const int hh = 1 << lg;
+#pragma unroll
+                for (int kk = 0; kk < kQe / 2; ++kk) {
+                    const int j = ((kk >> lg) << (lg + 1)) + (kk & (hh - 1));
+                    const float a = x[j], c = x[j + hh];
+                    x[j] = __fadd_rn(a, c);
+                    x[j + hh] = __fsub_rn(a, c);
+                }
+            }
+#pragma unroll
+            for (int st = 1; st <= 2; st <<= 1) {
+                const bool upper = (qq & st) != 0;
+#pragma unroll
+                for (int j = 0; j < kQe; ++j) {
+                    const float y = __shfl_xor_sync(0xffffffffu, x[j], st);
+                    x[j] = upper ? __fsub_rn(y, x[j]) : __fadd_rn(x[j], y);
+                }
+            }
+            float amax = 0.0f;
+#pragma unroll
+            for (int d = 0; d < kQe; ++d) amax = fmaxf(amax, fabsf(x[d]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            float s = 0.0f, rr = 0.0f;
+            if (amax != 0.0f) {
+                s = __fdiv_rn(amax, 448.0f);
+                rr = __fdiv_rn(448.0f, amax);
+            }
+            if (qq == 0) sq[qr] = s;
+            const int qg = qr & 127;                             // row of its 128-row group
+            uint8_t* qbase = sm + Sm::kQ + (qr >> 7) * (128 * Sm::kQRow);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t w4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int d = 16 * c + 4 * e;
+                    const uint32_t lo16 = e4m3x2_rn_satfinite(__fmul_rn(x[d], rr), __fmul_rn(x[d + 1], rr));
+                    const uint32_t hi16 = e4m3x2_rn_satfinite(__fmul_rn(x[d + 2], rr), __fmul_rn(x[d + 3], rr));
+                    w4[e] = amax != 0.0f ? (lo16 | (hi16 << 16)) : 0u;
+                }
+                const int chunk = (D / 64) * qq + c;
+                if constexpr (MX) {
+                    // the codes' exact bf16 values, channels ordered as the
+                    // converters order K's: pair m = (channel m, m + 4)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const int k8 = 2 * chunk + hh;
+                        const uint32_t wa = w4[2 * hh], wb = w4[2 * hh + 1];
+                        *reinterpret_cast<uint4*>(qbase + (k8 >> 3) * (128 * 128) + qg * 128 +
+                                                  (((k8 & 7) ^ (qg & 7)) << 4)) =
+                            make_uint4(e4m3_pick_to_bf16x2<0>(wa, wb), e4m3_pick_to_bf16x2<1>(wa, wb),
+                                       e4m3_pick_to_bf16x2<2>(wa, wb), e4m3_pick_to_bf16x2<3>(wa, wb));
+                    }
+                } else {
+                    *reinterpret_cast<uint4*>(qbase + qg * D + (e4m3_chunk<D>(chunk, qg) << 4)) =
+                        make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[Sm::kQReady]);
+        named_sync(1, 256);                          // every row's s_q is there
+
+        // base-2 logit = (S k_scale) cq; cq >= FLT_MIN keeps a masked -inf
+        const float cq = fmaxf(rv ? sq[r] * p.logit_scale_log2 : 0.0f, FLT_MIN);
+        const uint64_t cq2 = f2_pack(cq, cq);
+        const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+        const uint32_t ts = trow + 128 * g, to = trow + kOCol + 128 * g;
+        const bool idle = __all_sync(0xffffffffu, !rv);      // 32 rows of padding: the warp only keeps time
+        float m_run = -INFINITY;
+        uint64_t l2 = f2_pack(0.0f, 0.0f);
+        bool ok = true;
+        const int my_units = (nu - g + 1) / 2;
+        for (int k = 0; k < my_units; ++k) {
+            const int i = RG == 2 ? k : 2 * k + g, c = i % kScStages;
+            ok = warp_all(mbar_wait(&bars[Sm::kSFull + g], k & 1, abort_flag, &g_shared_err, 8));
+            if (ok) ok = warp_all(mbar_wait(&bars[Sm::kScFull + c], (i / kScStages) & 1, abort_flag, &g_shared_err, 9));
+            if (!ok) break;
+            if (!idle) {
+                tc_fence_after();
+                uint32_t x[128];
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) tmem_ld32(ts + 32 * cc, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * cc));
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(x + 32 * cc));
+                const int key0 = (tb + i) * kKeys;
+                const int badm = meta[c];
+                if constexpr (!MX) {
+                    const float4* ks = reinterpret_cast<const float4*>(scl + c * Sm::kScSlot);
+#pragma unroll
+                    for (int k4 = 0; k4 < 32; ++k4) {
+                        const float4 s = ks[k4];
+                        float a, b;
+                        f2_unpack(f2_mul(f2_pack(__uint_as_float(x[4 * k4]), __uint_as_float(x[4 * k4 + 1])),
+                                         f2_pack(s.x, s.y)), a, b);
+                        x[4 * k4] = __float_as_uint(a);
+                        x[4 * k4 + 1] = __float_as_uint(b);
+                        f2_unpack(f2_mul(f2_pack(__uint_as_float(x[4 * k4 + 2]), __uint_as_float(x[4 * k4 + 3])),
+                                         f2_pack(s.z, s.w)), a, b);
+                        x[4 * k4 + 2] = __float_as_uint(a);
+                        x[4 * k4 + 3] = __float_as_uint(b);
+                    }
+                }
+                // a tile inside every row's window with no bad page needs no mask
+                if (!__all_sync(0xffffffffu, key0 >= key_lo && key0 + kKeys - 1 <= key_hi && badm == 0)) {
+                    const int clo = key_lo - key0, chi = key_hi - key0;
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j < clo || j > chi || ((badm >> (j >> p.lg_page)) & 1)) x[j] = 0xFF800000u;   // -inf
+                }
+                float m4[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) m4[q] = fmax3(__uint_as_float(x[q]), __uint_as_float(x[q + 4]), __uint_as_float(x[q + 8]));
+#pragma unroll
+                for (int j = 12; j + 8 <= 124; j += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], __uint_as_float(x[j + q]), __uint_as_float(x[j + q + 4]));
+#pragma unroll
+                for (int q = 0; q < 4; ++q) m4[q] = fmaxf(m4[q], __uint_as_float(x[124 + q]));
+                float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                mx = mx == -INFINITY ? -INFINITY : mx * cq;
+                float alpha = 1.0f;
+                const bool raise = mx > m_run + kLazyMax || (m_run == -INFINITY && mx > -INFINITY);
+                if (raise) {
+                    alpha = m_run == -INFINITY ? 1.0f : ex2_approx(m_run - mx);
+                    l2 = f2_mul(l2, f2_pack(alpha, alpha));
+                    m_run = mx;
+                }
+                const bool resc = alpha != 1.0f;
+                const float sub = m_run == -INFINITY ? 0.0f : m_run;
+                const uint64_t nsub2 = f2_pack(-sub, -sub);
+                const float4* vs = reinterpret_cast<const float4*>(scl + c * Sm::kScSlot + kKeys);
+#pragma unroll
+                for (int cc = 0; cc < 4; ++cc) {              // 32 keys -> 16 columns of P
+                    uint32_t w[16];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int j = 32 * cc + 4 * q;
+                        float e0, e1, e2, e3;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), cq2, nsub2), e0, e1);
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])), cq2, nsub2), e2, e3);
+                        uint64_t p01 = f2_pack(ex2_approx(e0), ex2_approx(e1));
+                        uint64_t p23 = f2_pack(ex2_approx(e2), ex2_approx(e3));
+                        l2 = f2_add(l2, f2_add(p01, p23));
+                        if constexpr (!MX) {
+                            const float4 v = vs[8 * cc + q];
+                            p01 = f2_mul(p01, f2_pack(v.x, v.y));
+                            p23 = f2_mul(p23, f2_pack(v.z, v.w));
+                        }
+                        f2_unpack(p01, e0, e1);
+                        f2_unpack(p23, e2, e3);
+                        const __nv_bfloat162 b01 = __floats2bfloat162_rn(e0, e1), b23 = __floats2bfloat162_rn(e2, e3);
+                        w[2 * q] = *reinterpret_cast<const uint32_t*>(&b01);
+                        w[2 * q + 1] = *reinterpret_cast<const uint32_t*>(&b23);
+                    }
+                    tmem_st16(ts + 16 * cc, w);
+                }
+                // O of the rows whose maximum was raised (PV of the group's
+                // last unit is done: S of this one was issued after it)
+                if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll
+                    for (int hf = 0; hf < D / 32; ++hf) {
+                        uint32_t o[32];
+                        tmem_ld32(to + 32 * hf, o);
+                        tmem_wait_ld(o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                        tmem_st32(to + 32 * hf, o);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars[Sm::kPReady + g]);
+                mbar_arrive(&bars[Sm::kScEmpty + c]);
+            }
+        }
+        if (ok && my_units > 0)
+            ok = warp_all(mbar_wait(&bars[Sm::kPvDone + g], (my_units - 1) & 1, abort_flag, &g_shared_err, 10));
+        float l0, l1;
+        f2_unpack(l2, l0, l1);
+        float l = l0 + l1;
+        if (!ok || my_units == 0 || m_run == -INFINITY) {
+            m_run = -INFINITY;
+            l = 0.0f;
+        }
+        tc_fence_after();
+        // channel of TMEM column j (MX: the order of the converted V rows)
+        auto chan = [](int j) { return MX ? (j & ~7) + ((j >> 1) & 3) + 4 * (j & 1) : j; };
+        float* po = p.o + part * D * kRowsCta + r;
+        if constexpr (RG == 2) {
+            p.stat[part * kRowsCta + r] = make_float2(m_run, l);
+            if (my_units > 0 && !idle) {
+#pragma unroll
+                for (int hf = 0; hf < D / 32; ++hf) {
+                    uint32_t o[32];
+                    tmem_ld32(to + 32 * hf, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) po[chan(32 * hf + j) * kRowsCta] = __uint_as_float(o[j]);
+                }
+            }
+            tc_fence_before();
+        } else {
+            // each group hands the half of O that the other one finishes to it
+            float2* xs = reinterpret_cast<float2*>(sm + Sm::kXStat);
+            float* xo = reinterpret_cast<float*>(sm + Sm::kX);
+            tc_fence_before();
+            bar_sync_all(kThreads);                  // the code stages are free
+            tc_fence_after();
+            xs[128 * g + r] = make_float2(m_run, l);
+            const int give = (D / 2) * (1 - g), keep = (D / 2) * g;
+            if (my_units > 0 && !idle) {
+#pragma unroll
+                for (int hf = 0; hf < D / 64; ++hf) {
+                    uint32_t o[32];
+                    tmem_ld32(to + give + 32 * hf, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) xo[(give + 32 * hf + j) * 128 + r] = __uint_as_float(o[j]);
+                }
+            }
+            named_sync(1, 256);
+            const float2 other = xs[128 * (1 - g) + r];
+            const float M = fmaxf(m_run, other.x);
+            const float wa = m_run == -INFINITY ? 0.0f : ex2_approx(m_run - M);
+            const float wb = other.x == -INFINITY ? 0.0f : ex2_approx(other.x - M);
+            if (g == 0) p.stat[part * 128 + r] = make_float2(M, wa * l + wb * other.y);
+            if (nt > 0 && !idle) {
+#pragma unroll
+                for (int hf = 0; hf < D / 64; ++hf) {
+                    uint32_t o[32];
+                    tmem_ld32(to + keep + 32 * hf, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int col = keep + 32 * hf + j;
+                        // (a group without a key in the row has no O)
+                        float y = m_run == -INFINITY ? 0.0f : wa * __uint_as_float(o[j]);
+                        if (other.x != -INFINITY) y = fmaf(wb, xo[col * 128 + r], y);
+                        po[chan(col) * 128] = y;
+                    }
+                }
+            }
+            tc_fence_before();
+        }
+    } else {
+      reg_dealloc<kRegsConv>();
+        // ------------------------------------------------------------ converters
+        // lane -> cache row (key; V^T: channel) 32 cw + lane of the tile
+        const int row = 32 * (warp - kConvWarp0) + lane;
+        for (int i = 0; i < nt; ++i) {
+            const int s = i % kStages, vb = i & 1;
+            bool ok = warp_all(mbar_wait(&bars[Sm::kKvFull + s], (i / kStages) & 1, abort_flag, &g_shared_err, 11));
+            if constexpr (MX) {
+                if (ok && i >= 1) ok = warp_all(mbar_wait(&bars[Sm::kKbFree], (i - 1) & 1, abort_flag, &g_shared_err, 12));
+                if (!ok) break;
+                const uint8_t* krow = sm + Sm::kK + s * Sm::kKStage + row * 64;
+                const uint32_t esc = *reinterpret_cast<const uint32_t*>(sm + Sm::kKsf + s * Sm::kSfStage + row * 4);
+                uint8_t* dst = sm + Sm::kKb + row * 128;
+#pragma unroll
+                for (int blk = 0; blk < 4; ++blk) {
+                    uint32_t o[16];
+                    e2m1_block_to_bf16(*reinterpret_cast<const uint4*>(krow + (e4m3_chunk<64>(blk, row) << 4)),
+                                       (esc >> (8 * blk)) & 0xFFu, o);
+                    uint8_t* atom = dst + (blk >> 1) * (kKeys * 128);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4*>(atom + (((4 * (blk & 1) + q) ^ (row & 7)) << 4)) =
+                            make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[Sm::kKbReady]);
+            }
+            if (ok && i >= 2) ok = warp_all(mbar_wait(&bars[Sm::kVFree + vb], ((i - 2) >> 1) & 1, abort_flag, &g_shared_err, 13));
+            if (!ok) break;
+            uint8_t* dst = sm + Sm::kVb + vb * Sm::kVbBuf + row * 128;
+            if constexpr (MX) {
+                const uint8_t* vrow = sm + Sm::kV + s * Sm::kKStage + row * 64;
+                const uint32_t esc = *reinterpret_cast<const uint32_t*>(sm + Sm::kVsf + s * Sm::kSfStage + row * 4);
+#pragma unroll
+                for (int blk = 0; blk < 4; ++blk) {
+                    uint32_t o[16];
+                    e2m1_block_to_bf16(*reinterpret_cast<const uint4*>(vrow + (e4m3_chunk<64>(blk, row) << 4)),
+                                       (esc >> (8 * blk)) & 0xFFu, o);
+                    uint8_t* atom = dst + (blk >> 1) * (kKeys * 128);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4*>(atom + (((4 * (blk & 1) + q) ^ (row & 7)) << 4)) =
+                            make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                }
+            } else {
+                // 16-byte chunk c of the code row (V: 16 channels of a key;
+                // V^T: 16 keys of a channel) -> two chunks of the bf16 row
+                const int width = p.v_trans ? kKeys : D;
+                const uint8_t* vrow = sm + Sm::kV + s * Sm::kKStage + row * width;
+                const int atom_b = p.v_trans ? D * 128 : kKeys * 128;
+                if (!p.v_trans || row < D) {
+#pragma unroll 4
+                    for (int c = 0; c < width / 16; ++c) {
+                        const int at = width == 128 ? (c ^ (row & 7)) : (c ^ ((row >> 1) & 3));
+                        const uint4 u = *reinterpret_cast<const uint4*>(vrow + (at << 4));
+                        uint8_t* half = dst + (c >> 2) * atom_b;
+                        const int ch = 2 * (c & 3);
+                        *reinterpret_cast<uint4*>(half + ((ch ^ (row & 7)) << 4)) =
+                            make_uint4(e4m3x2_to_bf16x2(u.x, 0x1404u), e4m3x2_to_bf16x2(u.x, 0x3424u),
+                                       e4m3x2_to_bf16x2(u.y, 0x1404u), e4m3x2_to_bf16x2(u.y, 0x3424u));
+                        *reinterpret_cast<uint4*>(half + (((ch + 1) ^ (row & 7)) << 4)) =
+                            make_uint4(e4m3x2_to_bf16x2(u.z, 0x1404u), e4m3x2_to_bf16x2(u.z, 0x3424u),
+                                       e4m3x2_to_bf16x2(u.w, 0x1404u), e4m3x2_to_bf16x2(u.w, 0x3424u));
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&bars[Sm::kVReady + vb]);
+                mbar_arrive(&bars[Sm::kKvEmpty + s]);
+            }
+        }
+    }
+    __syncwarp();
+    if (RG == 1 && warp >= 8) bar_sync_all(kThreads);            // (the softmax warps were there above)
+    __syncwarp();
+    tc_fence_before();
+    bar_sync_all(kThreads);
+    if (warp == kMmaWarp) {                          // TMEM is read by nobody any more
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // ------------------------------------------------------------------ launch
 
 // Where the partials of the two parts lie in the workspace.
@@ -131,7 +864,7 @@ struct SharedPlan {
 SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
     SharedPlan w;
     const int64_t rows = (int64_t)B * T * (H / Hk);
-    w.pre_rows = kFewRows;
+    w.pre_rows = rows <= kFewRows ? kFewRows : (rows <= 256 ? 128 : 256);
     w.n_rt = (int)ceil_div(rows, w.pre_rows);
     const int sms = device_sms();
     w.np = (int)std::max<int64_t>(1, sms / ((int64_t)w.n_rt * Hk));
@@ -143,6 +876,55 @@ SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
     w.own_o = w.pre_o + pre * D * sizeof(float);
     w.bytes = w.own_o + own * D * sizeof(float);
     return w;
+}
+
+template <int D, bool MX, int RG>
+cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, const SharedPart& part, cudaStream_t s) {
+    const DecodeArgs& a = sa.d;
+    constexpr int kSmem = SmP<D, MX, RG>::kBytes + 1024;
+    PrefixParams p = {};
+    p.q = static_cast<const uint16_t*>(a.q.ptr);
+    p.qs0 = a.q.stride[0];
+    p.qs1 = a.q.stride[1];
+    p.qs2 = a.q.stride[2];
+    p.qs3 = a.q.stride[3];
+    p.q_vec = view_vec8(a.q) ? 1 : 0;
+    p.ksc = a.k_scale;
+    p.vsc = a.v_scale;
+    p.per_tensor = (a.kv_flags & 1) ? 1 : 0;
+    p.v_trans = (!MX && (a.kv_flags & 2)) ? 1 : 0;
+    p.ksf8 = a.k_sf;
+    p.vsf8 = a.v_sf;
+    p.ptab = sa.prefix_table;
+    p.plen = sa.prefix_len;
+    p.ctx = a.ctx_lens;
+    p.T = a.T;
+    p.Hk = a.Hk;
+    p.G = a.H / a.Hk;
+    p.R = a.T * p.G;
+    p.n_rows = a.B * p.R;
+    p.page = a.page_size;
+    p.lg_page = 31 - __builtin_clz(static_cast<unsigned>(a.page_size));
+    p.cap_prefix = sa.max_prefix_pages * a.page_size;
+    p.cap_rows = a.max_pages * a.page_size;
+    p.num_pages = a.num_pages;
+    p.window = a.window;
+    p.np = w.np;
+    p.n_rt = w.n_rt;
+    p.logit_scale_log2 = a.softmax_scale / static_cast<float>(D) * kLog2e;
+    p.stat = part.stat;
+    p.o = part.o;
+    CUtensorMap tk, tv;
+    const bool ok = MX ? encode_cache_mx(&tk, a.k_cache, a.num_pages, a.Hk, a.page_size, D) &&
+                             encode_cache_mx(&tv, a.v_cache, a.num_pages, a.Hk, a.page_size, D)
+                       : encode_cache(&tk, a.k_cache, a.num_pages, a.Hk, a.page_size, D) &&
+                             (p.v_trans ? encode_cache_vt(&tv, a.v_cache, a.num_pages, a.Hk, D)
+                                        : encode_cache(&tv, a.v_cache, a.num_pages, a.Hk, a.page_size, D));
+    if (!ok) return cudaErrorInvalidValue;
+    auto kern = prefix_kernel<D, MX, RG>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(w.np, w.n_rt * a.Hk), dim3(kThreads), kSmem, s, tk, tv, p);
 }
 
 }  // namespace
@@ -162,7 +944,18 @@ cudaError_t launch_decode_shared(const DecodeSharedArgs& sa, cudaStream_t s) {
     part.n_rt = w.n_rt;
     part.stat = reinterpret_cast<float2*>(ws + w.pre_stat);
     part.o = reinterpret_cast<float*>(ws + w.pre_o);
-    cudaError_t e = launch_decode_part(a, part, s);
+    cudaError_t e;
+    if (w.pre_rows == kFewRows) {
+        e = launch_decode_part(a, part, s);
+    } else if (w.pre_rows == 128) {
+        e = a.mx ? launch_prefix<128, true, 1>(sa, w, part, s)
+                 : (a.D == 128 ? launch_prefix<128, false, 1>(sa, w, part, s)
+                               : launch_prefix<64, false, 1>(sa, w, part, s));
+    } else {
+        e = a.mx ? launch_prefix<128, true, 2>(sa, w, part, s)
+                 : (a.D == 128 ? launch_prefix<128, false, 2>(sa, w, part, s)
+                               : launch_prefix<64, false, 2>(sa, w, part, s));
+    }
     if (e != cudaSuccess) return e;
     MergeParams m = {};
     m.pre_stat = part.stat;
