@@ -209,13 +209,6 @@ struct DecParams {
     int o_vec;                               // out rows: 4 channels as one 8-byte store
     const uint8_t* ksf8;                     // MX: e8m0 block scales [num_pages, Hk, page, D / 32]
     const uint8_t* vsf8;
-    // SHARED: the batch's sequences begin with the same *plen tokens
-    const int32_t* plen;
-    int cap_prefix;                          // tokens the prefix table has room for
-    int pre;                                 // 1: rows of all sequences against the prefix, 0: own keys
-    int cap_rows;                            // pre: tokens a sequence's table has room for
-    int late_wait;                           // nothing here depends on the preceding kernel: wait for it last
-    int n_rows, n_rt;                        // pre: B T G rows of a kv head, 64-row tiles of them
     float2* ws_stat;                         // nsplit > 1: partial (m, l) [B Hk][nsplit][64]
     float* ws_o;                             //   and partial O [B Hk][nsplit][64][128] fp32
 };
@@ -256,11 +249,7 @@ __device__ __forceinline__ void store_out4(const DecParams& p, int b, int hk, in
 // logits instead of one warp holding them all. Each A row keeps its own
 // running max, sum and O rows; the NREP rows of a query row are combined
 // (log-sum-exp) with the two groups' when the CTA's result is written.
-// SHARED: the pass over one part of a batch that shares a prefix, its
-// partials always left in the workspace. p.pre: CTA = 64 of the B T G query
-// rows of kv head hk (row n = (b T + t) G + g) against the keys [0, L) of the
-// prefix's pages; else rows of one sequence against its own keys [L, ctx).
-template <int D, bool MX, int NREP, bool SHARED>
+template <int D, bool MX, int NREP>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const DecParams p) {
@@ -286,15 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int split = blockIdx.x;
     const int bhk = blockIdx.y;
-    const bool pre = SHARED && p.pre;
-    const int b = pre ? 0 : bhk / p.Hk, hk = pre ? bhk / p.n_rt : bhk % p.Hk;
-    const int row0 = pre ? (bhk % p.n_rt) * kRows : 0;
-    const int R = pre ? min(kRows, p.n_rows - row0) : p.R;
+    const int b = bhk / p.Hk, hk = bhk % p.Hk;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // sequence and query token of row r, its query head
-    auto row_b = [&](int r) { return pre ? (row0 + r) / p.R : b; };
-    auto row_t = [&](int r) { return pre ? (row0 + r) % p.R / p.G : r / p.G; };
-    auto row_h = [&](int r) { return hk * p.G + (pre ? (row0 + r) % p.G : r % p.G); };
 
     // setup that reads no global memory (barriers, TMEM, the tensor maps of
     // the parameter space) overlaps the preceding kernel in the stream when
@@ -302,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // griddepcontrol.wait sees that kernel's writes
     // softmax warps per group that hold query rows (the others, whose 16
     // rows are all padding, take no part in the tile loop)
-    const int n_act = NREP > 1 ? 4 : min(4, (R + 15) >> 4);
+    const int n_act = NREP > 1 ? 4 : min(4, (p.R + 15) >> 4);
     if (warp == kIdleWarp) {
         for (int i = lane; i < Sm::kNumBars; i += 32) {
             uint32_t cnt = 1;                                       // expect_tx; commits
@@ -325,18 +307,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    if (!(SHARED && p.late_wait)) pdl_wait();
+    pdl_wait();
     pdl_launch_dependents();
 
-    int L = 0;                                       // SHARED: the prefix's length
-    if constexpr (SHARED) {
-        L = *p.plen;
-        if (L > p.cap_prefix || L < 0) {
-            if (tid == 0 && split == 0) atomicCAS(&g_decode_err, 0u, kErrDecodeRange);
-            L = max(0, min(L, p.cap_prefix));
-        }
-    }
-    int ctx = pre ? L : p.ctx[b];
+    int ctx = p.ctx[b];
     const int cap = p.max_pages * p.page;
     if (ctx > cap || ctx < 0) {
         if (tid == 0 && split == 0) atomicCAS(&g_decode_err, 0u, kErrDecodeRange);
@@ -344,14 +318,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // keys [lo, ctx) as 128-key tiles [t0, t1) at absolute positions; this
     // CTA's share is [tb, tb + nt)
-    const int lo = pre ? 0 : max(SHARED ? L : 0, ctx - p.T - p.window + 1);
-    const int t0 = lo / kKeys, t1 = SHARED && lo >= ctx ? t0 : (ctx + kKeys - 1) / kKeys;
+    const int lo = max(0, ctx - p.T - p.window + 1);
+    const int t0 = lo / kKeys, t1 = (ctx + kKeys - 1) / kKeys;
     const int n_all = max(0, t1 - t0);
-    // SHARED: no split gets fewer than kMinTiles tiles while another has any
-    const int nsp = SHARED ? shared_splits(n_all, p.nsplit) : p.nsplit;
-    const int sp = SHARED ? min(split, nsp) : split, sp1 = SHARED ? min(split + 1, nsp) : split + 1;
-    const int tb = t0 + (sp * n_all) / nsp;
-    const int nt = t0 + (sp1 * n_all) / nsp - tb;
+    const int tb = t0 + (split * n_all) / p.nsplit;
+    const int nt = t0 + ((split + 1) * n_all) / p.nsplit - tb;
 
     // the producer's first page-table entries, requested before the barrier
     const int ppt = kKeys / p.page;                  // pages per tile (divides 32)
@@ -364,10 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the softmax warps' query row quarters (contiguous rows), also in flight
     // across the barrier
     uint4 qv[kQv] = {};
-    if (warp < kSoftWarps && p.q_vec && ((tid >> 2) % kPeriod) < R) {
+    if (warp < kSoftWarps && p.q_vec && ((tid >> 2) % kPeriod) < p.R) {
         const int r = (tid >> 2) % kPeriod;
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + row_b(r) * p.qs0 + row_t(r) * p.qs1 +
-                                                          row_h(r) * p.qs2) + kQv * (tid & 3);
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + b * p.qs0 + (r / p.G) * p.qs1 +
+                                                          (hk * p.G + r % p.G) * p.qs2) + kQv * (tid & 3);
 #pragma unroll
         for (int c = 0; c < kQv; ++c) qv[c] = __ldg(src + c);
     }
@@ -602,9 +573,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
             const int r = tid >> 2, qq = tid & 3;          // A row r holds query row rq
             const int rq = r % kPeriod;
-            const bool rv = rq < R;
-            const int t = rv ? row_t(rq) : 0, h = rv ? row_h(rq) : 0;
-            const uint16_t* src = p.q + (rv ? row_b(rq) : 0) * p.qs0 + t * p.qs1 + h * p.qs2 + (int64_t)(qq * kQe) * p.qs3;
+            const bool rv = rq < p.R;
+            const int t = rv ? rq / p.G : 0, h = rv ? hk * p.G + rq % p.G : 0;
+            const uint16_t* src = p.q + b * p.qs0 + t * p.qs1 + h * p.qs2 + (int64_t)(qq * kQe) * p.qs3;
             float x[kQe];
             if (p.q_vec) {
 #pragma unroll
@@ -716,16 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = 16 * qw + lr;
         const int rq = r % kPeriod;                       // its query row
         const int cb = (qw / (4 / NREP)) * (2 * kNC);
-        const bool rv = rq < R;
-        int ctx_row = ctx;
-        if (pre && rv) {
-            const int cap_row = p.cap_rows;
-            ctx_row = p.ctx[row_b(rq)];
-            ctx_row = max(0, min(ctx_row, cap_row));
-        }
-        const int pq = rv ? ctx_row - p.T + row_t(rq) : -1;    // the row's query position
-        // SHARED: the keys of this pass that the row sees
-        const int key_lo = max(pre ? 0 : L, pq - p.window + 1), key_hi = pre ? min(pq, L - 1) : pq;
+        const bool rv = rq < p.R;
+        const int pq = rv ? ctx - p.T + rq / p.G : -1;    // the row's query position
         // base-2 logit of a key = (acc * k_scale) * cq; cq kept >= FLT_MIN so
         // that a masked key (-inf) times cq stays -inf (a zero query row has
         // acc = 0, so its logits are 0 either way)
@@ -735,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m_run = -INFINITY;                      // the max O[g] and the sum are expressed against
         uint64_t lsum2 = f2_pack(0.0f, 0.0f);         // running sum as an f32x2 pair
         bool ok = true;
-        const int nt_mine = (NREP > 1 || 16 * qw < R) ? nt : 0;   // a warp of padding rows only sits out
+        const int nt_mine = (NREP > 1 || 16 * qw < p.R) ? nt : 0;   // a warp of padding rows only sits out
         for (int i = g; i < nt_mine; i += 2) {
             const int c = i % kScStages;
             ok = warp_all(mbar_wait(&bars[Sm::kSFull + g], (i >> 1) & 1, abort_flag, &g_decode_err, 5));
@@ -767,15 +730,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // masks: rows past R; keys outside the row's window; bad pages.
             // A tile inside every row's window with no bad page needs none.
-            const bool full = badm == 0 && (SHARED ? key0 >= key_lo && key0 + kKeys - 1 <= key_hi
-                                                   : key0 >= ctx - p.window && key0 + kKeys - 1 <= ctx - p.T);
+            const bool full = badm == 0 && key0 >= ctx - p.window && key0 + kKeys - 1 <= ctx - p.T;
             if (!rv) {
 #pragma unroll
                 for (int k = 0; k < kNC; ++k) x[k] = -INFINITY;
             } else if (!full) {
                 // the row sees keys [kc0 + clo, kc0 + chi] of this thread's
-                const int clo = (SHARED ? key_lo : pq - p.window + 1) - kc0 - cpar;
-                const int chi = (SHARED ? key_hi : pq) - kc0 - cpar;
+                const int clo = pq - p.window + 1 - kc0 - cpar, chi = pq - kc0 - cpar;
 #pragma unroll
                 for (int k = 0; k < kNC; ++k) x[k] = (2 * k >= clo && 2 * k <= chi) ? x[k] : -INFINITY;
                 if (badm != 0) {
@@ -959,37 +920,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return acc;
                 }
             };
-            if (!SHARED && p.nsplit == 1) {
+            if (p.nsplit == 1) {
                 // thread: one row, four channels
-                for (int idx = tid; idx < R * (kD / 4); idx += kSoftWarps * 32) {
+                for (int idx = tid; idx < p.R * (kD / 4); idx += kSoftWarps * 32) {
                     const int rr = idx / (kD / 4), d4 = 4 * (idx % (kD / 4));
                     const float2 st = row_stat(rr);
                     store_out4(p, b, hk, rr, d4, row_o4(rr, d4, st.x), st.y > 0.0f ? 1.0f / st.y : 0.0f);
                 }
             } else {
-                // the partial to the workspace, combined by a merge kernel
+                // the partial to the workspace, combined by decode_merge_kernel
                 const size_t part = (size_t)bhk * p.nsplit + split;
-                if constexpr (SHARED) {
-                    // channel-major [D][64 rows], as the merge over the parts
-                    // reads it; a part with no key leaves its statistics alone
-                    float* wo = p.ws_o + part * kRows * kD;
-                    const int work = nt == 0 ? 0 : R * (kD / 4);
-                    for (int idx = tid; idx < work; idx += kSoftWarps * 32) {
-                        const int rr = idx % R, d4 = 4 * (idx / R);
-                        const float4 o = row_o4(rr, d4, row_stat(rr).x);
-                        wo[d4 * kRows + rr] = o.x;
-                        wo[(d4 + 1) * kRows + rr] = o.y;
-                        wo[(d4 + 2) * kRows + rr] = o.z;
-                        wo[(d4 + 3) * kRows + rr] = o.w;
-                    }
-                } else {
-                    float4* wo = reinterpret_cast<float4*>(p.ws_o + part * kRows * kD);
-                    for (int idx = tid; idx < R * (kD / 4); idx += kSoftWarps * 32) {
-                        const int rr = idx / (kD / 4), d4 = 4 * (idx % (kD / 4));
-                        wo[idx] = row_o4(rr, d4, row_stat(rr).x);
-                    }
+                float4* wo = reinterpret_cast<float4*>(p.ws_o + part * kRows * kD);
+                for (int idx = tid; idx < p.R * (kD / 4); idx += kSoftWarps * 32) {
+                    const int rr = idx / (kD / 4), d4 = 4 * (idx % (kD / 4));
+                    wo[idx] = row_o4(rr, d4, row_stat(rr).x);
                 }
-                if (tid < R) p.ws_stat[part * kRows + tid] = row_stat(tid);
+                if (tid < p.R) p.ws_stat[part * kRows + tid] = row_stat(tid);
             }
         }
     } else {
@@ -1115,7 +1061,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         bar_sync_all(kThreads);
     }
-    if (SHARED && p.late_wait) pdl_wait();       // this grid ends after the one before it
 }
 
 // The splits of (b, hk) combined (log-sum-exp): thread = one query row and
@@ -1201,10 +1146,10 @@ size_t decode_ws_bytes(int B, int, int, int Hk, int D, int) {
 
 namespace {
 
-// The parameters and tensor maps that every launch on one cache shares.
 template <int D, bool MX>
-cudaError_t decode_setup(const DecodeArgs& a, DecParams& p, CUtensorMap& tk, CUtensorMap& tv) {
-    p = {};
+cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t s) {
+    constexpr int kSmemBytes = smem_bytes<D, MX>();
+    DecParams p;
     p.q = static_cast<const uint16_t*>(a.q.ptr);
     p.qs0 = a.q.stride[0];
     p.qs1 = a.q.stride[1];
@@ -1240,6 +1185,7 @@ cudaError_t decode_setup(const DecodeArgs& a, DecParams& p, CUtensorMap& tk, CUt
                a.q.stride[2] % 8 == 0 && reinterpret_cast<uintptr_t>(a.q.ptr) % 16 == 0)
                   ? 1
                   : 0;
+    CUtensorMap tk, tv;
     if (MX) {
         if (!encode_cache_mx(&tk, a.k_cache, a.num_pages, a.Hk, a.page_size, D) ||
             !encode_cache_mx(&tv, a.v_cache, a.num_pages, a.Hk, a.page_size, D))
@@ -1249,26 +1195,17 @@ cudaError_t decode_setup(const DecodeArgs& a, DecParams& p, CUtensorMap& tk, CUt
                            : encode_cache(&tv, a.v_cache, a.num_pages, a.Hk, a.page_size, D))) {
         return cudaErrorInvalidValue;
     }
+    const int nrep = pick_nrep(p.R);
+    auto kern = nrep == 4 ? decode_kernel<D, MX, 4> : (nrep == 2 ? decode_kernel<D, MX, 2> : decode_kernel<D, MX, 1>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    p.nsplit = pick_nsplit(a.B * a.Hk, a.T, a.window, a.page_size, a.max_pages);
     p.o_vec = (a.out_stride[3] == 1 && a.out_stride[0] % 4 == 0 && a.out_stride[1] % 4 == 0 &&
                a.out_stride[2] % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % 8 == 0)
                   ? 1
                   : 0;
-    return cudaSuccess;
-}
-
-template <int D, bool MX>
-cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t s) {
-    constexpr int kSmemBytes = smem_bytes<D, MX>();
-    DecParams p;
-    CUtensorMap tk, tv;
-    cudaError_t e = decode_setup<D, MX>(a, p, tk, tv);
-    if (e != cudaSuccess) return e;
-    const int nrep = pick_nrep(p.R);
-    auto kern = nrep == 4 ? decode_kernel<D, MX, 4, false>
-                          : (nrep == 2 ? decode_kernel<D, MX, 2, false> : decode_kernel<D, MX, 1, false>);
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    p.nsplit = pick_nsplit(a.B * a.Hk, a.T, a.window, a.page_size, a.max_pages);
+    p.ws_stat = nullptr;
+    p.ws_o = nullptr;
     if (p.nsplit > 1) {
         if (a.ws == nullptr) return cudaErrorInvalidValue;
         p.ws_stat = static_cast<float2*>(a.ws);
@@ -1295,46 +1232,7 @@ cudaError_t launch_decode_d(const DecodeArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <int D, bool MX>
-cudaError_t launch_part_d(const DecodeArgs& a, const SharedPart& sp, cudaStream_t s) {
-    constexpr int kSmemBytes = smem_bytes<D, MX>();
-    DecParams p;
-    CUtensorMap tk, tv;
-    cudaError_t e = decode_setup<D, MX>(a, p, tk, tv);
-    if (e != cudaSuccess) return e;
-    p.plen = sp.prefix_len;
-    p.cap_prefix = sp.max_prefix_pages * a.page_size;
-    p.cap_rows = a.max_pages * a.page_size;
-    p.n_rows = a.B * p.R;
-    p.n_rt = sp.n_rt;
-    p.nsplit = sp.nsplit;
-    p.ws_stat = sp.stat;
-    p.ws_o = sp.o;
-    p.pre = sp.pre;
-    p.late_wait = sp.late_wait;
-    if (sp.pre) {
-        p.ptab = sp.prefix_table;
-        p.max_pages = sp.max_prefix_pages;
-    }
-    const int nrep = pick_nrep(sp.pre ? std::min(p.n_rows, kRows) : p.R);
-    auto kern = nrep == 4 ? decode_kernel<D, MX, 4, true>
-                          : (nrep == 2 ? decode_kernel<D, MX, 2, true> : decode_kernel<D, MX, 1, true>);
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(sp.nsplit, sp.pre ? sp.n_rt * a.Hk : a.B * a.Hk), dim3(kThreads), kSmemBytes, s, tk,
-                      tv, p);
-}
-
 }  // namespace
-
-cudaError_t launch_decode_part(const DecodeArgs& a, const SharedPart& p, cudaStream_t s) {
-    if (a.mx) return a.D == 128 ? launch_part_d<128, true>(a, p, s) : cudaErrorInvalidValue;
-    switch (a.D) {
-        case 64: return launch_part_d<64, false>(a, p, s);
-        case 128: return launch_part_d<128, false>(a, p, s);
-        default: return cudaErrorInvalidValue;
-    }
-}
 
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s) {
     if (a.mx) return a.D == 128 ? launch_decode_d<128, true>(a, s) : cudaErrorInvalidValue;

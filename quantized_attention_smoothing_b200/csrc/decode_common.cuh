@@ -17,15 +17,6 @@ namespace sage {
 namespace dec {
 
 constexpr int kKeys = 128;                   // keys per tile
-// Parts of a shared-prefix batch: the splits, of at most nsplit, that n_tiles
-// key tiles are shared out among. A CTA keeps two tiles in flight, so fewer
-// than kMinTiles each would only make more partials to combine.
-constexpr int kMinTiles = 2;
-__host__ __device__ inline int shared_splits(int n_tiles, int nsplit) {
-    const int want = (n_tiles + kMinTiles - 1) / kMinTiles;
-    return want < 1 ? 1 : (want < nsplit ? want : nsplit);
-}
-
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Head size D (64 or 128): an e4m3 row of Q, K or V is D bytes, stored

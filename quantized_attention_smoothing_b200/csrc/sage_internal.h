@@ -147,22 +147,6 @@ size_t decode_ws_bytes(int B, int T, int H, int Hk, int D, int window);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 unsigned read_clear_decode_error();
 unsigned read_clear_decode_error();
-// One part of the decode of a batch that shares a prefix: the query rows of
-// all sequences against the prefix's keys [0, *prefix_len) (pre), 64 rows a
-// CTA, or each sequence's against its own [*prefix_len, ctx). Every CTA leaves
-// its (m, l) [64] and O [D][64] (fp32, expressed against m) in the workspace.
-struct SharedPart {
-    int pre;
-    const int32_t* prefix_table;
-    const int32_t* prefix_len;
-    int max_prefix_pages;
-    int nsplit, n_rt;                       // CTAs per tile; pre: 64-row tiles of a kv head
-    float2* stat;
-    float* o;
-    int late_wait;                          // does not read what the preceding kernel writes
-};
-cudaError_t launch_decode_part(const DecodeArgs& a, const SharedPart& p, cudaStream_t s);
-
 // ---- decode of a batch that shares a prefix (shared.cu)
 struct DecodeSharedArgs {
     DecodeArgs d;

@@ -6,13 +6,13 @@
 // exp2(x - m), sum of exp2(x - m) v) of each part, the whole is
 //   M = max m_i,  out = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 // So every part of every row may be computed anywhere, and the launches are
-//   1. the prefix's keys against the B T G rows of each kv head: with few rows
-//      (at most 64) decode.cu's kernel, its rows taken across sequences; else
-//      prefix_kernel below, 128 or 256 rows a CTA;
-//   2. each sequence's own keys, decode.cu's kernel with keys from L on; it
-//      reads nothing of 1, so its CTAs start as those of 1 leave;
-//   3. shared_merge_kernel.
-// What bounds 1: reading K and V once is cheap (the point of the operator);
+//   1. query_kernel: the query rows rotated and quantised;
+//   2. prefix_kernel: the prefix's keys against the B T G rows of each kv head,
+//      128 or 256 rows a CTA (with at most 64 rows, rows_kernel does this);
+//   3. rows_kernel: each sequence's own keys; it reads nothing of 2, so its
+//      CTAs start as those of 2 leave;
+//   4. shared_merge_kernel.
+// What bounds 2: reading K and V once is cheap (the point of the operator);
 // for rows R and keys L the SMs do 2 R L D FP8 + 2 R L D bf16 MACs and R L
 // exponentials. At 128 rows x 128 keys that is 256 + 512 tensor cycles and
 // 1024 MUFU cycles an SM, so the exponential bounds a full tile and the two
@@ -24,6 +24,7 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "decode_common.cuh"
 #include "sage_internal.h"
@@ -36,7 +37,67 @@ using namespace dec;
 
 __device__ unsigned g_shared_err;
 
-constexpr int kFewRows = 64;                 // rows that decode.cu's kernel takes
+constexpr int kFewRows = 64;                 // rows that rows_kernel takes
+
+// The splits, of at most nsplit, that n key tiles (prefix_kernel) or blocks
+// (rows_kernel) are shared out among: none gets fewer than a CTA works on at
+// once, which would only make more partials to combine.
+__host__ __device__ inline int used_splits(int n, int nsplit, int at_once) {
+    const int want = (n + at_once - 1) / at_once;
+    return want < 1 ? 1 : (want < nsplit ? want : nsplit);
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// 2^e for |e| <= 252 (two normal factors, so that no half of it underflows).
+__device__ __forceinline__ float pow2i(int e) {
+    const int a = e / 2, b = e - a;
+    return __int_as_float((a + 127) << 23) * __int_as_float((b + 127) << 23);
+}
+
+// The e4m3 pair in the low (high) half of w as an fp16 pair, exactly.
+__device__ __forceinline__ uint32_t e4m3_lo_to_f16x2(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi_to_f16x2(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+// A mask of the n lowest bytes of a word (n <= 0: none, n >= 4: all).
+__device__ __forceinline__ uint32_t low_bytes(int n) {
+    return n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u);
+}
+
+// An FP8 cache's value scales are taken relative to a power of two, 2^e, so
+// that the weights p v_scale 2^-e fit fp16 (they keep 11 bits down to 2^-14;
+// bf16 would keep 8): e is the exponent of the first tile's largest scale and
+// is raised when a later tile has one over 2^kScaleRoom times as large, O
+// following by an exact power of two. Slots that hold no key of the part
+// count as zero, whatever they hold.
+constexpr int kScaleRoom = 4;
+constexpr int kNoExp = -1000;
+// The exponent to use from a tile on whose largest scale is vmax.
+__device__ __forceinline__ int scale_exp(int e, float vmax) {
+    const int ev = vmax > 0.0f ? max(-120, min(120, (int)(__float_as_uint(vmax) >> 23) - 126)) : kNoExp;
+    return ev > (e == kNoExp ? kNoExp : e + kScaleRoom) ? ev : e;
+}
+
+// The running max is only raised when a row's new maximum exceeds it by more
+// than this (base 2): p then stays below 2^8, which fp32 sums and 16-bit
+// weights hold as exactly as values below one, and most tiles leave O alone.
+constexpr float kLazyMax = 8.0f;
 
 // ------------------------------------------------------------------- merge
 
@@ -47,6 +108,7 @@ struct MergeParams {
     const float* own_o;                      // [B Hk][ns][D][64]
     const int32_t* plen;
     int cap_prefix, np, ns, pre_rows, n_rt;
+    int unit, at_once;                       // keys of a tile or block of the prefix part, used_splits' third
     int n_rows, R, T, G, Hk;
     __nv_bfloat16* out;
     int64_t os0, os1, os2, os3;
@@ -68,28 +130,46 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) 
     const int nn = in ? n : p.n_rows - 1;
     const int b = nn / p.R, rr = nn % p.R;
     const int L = max(0, min(*p.plen, p.cap_prefix));
-    const int np = L > 0 ? shared_splits((L + kKeys - 1) / kKeys, p.np) : 0;
+    const int np = L > 0 ? used_splits((L + p.unit - 1) / p.unit, p.np, p.at_once) : 0;
     const size_t part_p = ((size_t)hk * p.n_rt + nn / p.pre_rows) * p.np, part_o = ((size_t)b * p.Hk + hk) * p.ns;
     const int r = nn % p.pre_rows;
     float M = -INFINITY, l = 0.0f, acc[kCh];
 #pragma unroll
     for (int k = 0; k < kCh; ++k) acc[k] = 0.0f;
-    for (int e = warp; e < np + p.ns; e += 8) {
-        const bool pre = e < np;
-        const size_t part = pre ? part_p + e : part_o + (e - np);
-        const int rows = pre ? p.pre_rows : 64, row = pre ? r : rr;
-        const float2 s = __ldcg((pre ? p.pre_stat : p.own_stat) + part * rows + row);
-        const float* o = (pre ? p.pre_o : p.own_o) + (part * D + d0) * rows + row;
-        float v[kCh];
+    // kAtOnce parts at a time: their statistics, then the O of those that have keys
+    constexpr int kAtOnce = 4;
+    for (int e0 = warp; e0 < np + p.ns; e0 += 8 * kAtOnce) {
+        float2 s[kAtOnce];
+        float v[kAtOnce][kCh];
 #pragma unroll
-        for (int k = 0; k < kCh; ++k) v[k] = __ldcg(o + k * rows);
-        if (s.x == -INFINITY) continue;          // (a part without keys has no O)
-        const float m = fmaxf(M, s.x);
-        const float wa = M == -INFINITY ? 0.0f : ex2_approx(M - m), wb = ex2_approx(s.x - m);
-        l = fmaf(l, wa, wb * s.y);
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int e = e0 + 8 * i;
+            s[i] = make_float2(-INFINITY, 0.0f);
+            if (e < np) s[i] = __ldcg(p.pre_stat + (part_p + e) * p.pre_rows + r);
+            else if (e < np + p.ns) s[i] = __ldcg(p.own_stat + (part_o + e - np) * 64 + rr);
+        }
 #pragma unroll
-        for (int k = 0; k < kCh; ++k) acc[k] = fmaf(acc[k], wa, wb * v[k]);
-        M = m;
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int e = e0 + 8 * i;
+            const bool pre = e < np;
+            const int rows = pre ? p.pre_rows : 64;
+            const float* o = pre ? p.pre_o + ((part_p + e) * D + d0) * rows + r
+                                 : p.own_o + ((part_o + e - np) * D + d0) * rows + rr;
+            if (s[i].x != -INFINITY) {
+#pragma unroll
+                for (int k = 0; k < kCh; ++k) v[i][k] = __ldcg(o + k * rows);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            if (s[i].x == -INFINITY) continue;
+            const float m = fmaxf(M, s[i].x);
+            const float wa = M == -INFINITY ? 0.0f : ex2_approx(M - m), wb = ex2_approx(s[i].x - m);
+            l = fmaf(l, wa, wb * s[i].y);
+#pragma unroll
+            for (int k = 0; k < kCh; ++k) acc[k] = fmaf(acc[k], wa, wb * v[i][k]);
+            M = m;
+        }
     }
     st[warp][lane] = make_float2(M, l);
     __syncthreads();
@@ -123,10 +203,10 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) 
 
 // ------------------------------------------------------------------ prefix
 
-// The query rows of every sequence as the A operand of QK, once for all CTAs:
-// row n = (b T + t) G + g of kv head hk rotated (fp32 butterfly) and quantised
-// to e4m3 with scale max|q_hat| / 448 (the operations of decode.cu), written
-// as images of the shared-memory operand: per 128-row tile [128][D] codes in
+// The query rows of every sequence, once for all CTAs: row n = (b T + t) G + g
+// of kv head hk rotated (fp32 butterfly) and quantised to e4m3 with scale
+// max|q_hat| / 448 (the operations of decode.cu). The codes go out row by row
+// for rows_kernel, and for prefix_kernel as images of its shared-memory operand: per 128-row tile [128][D] codes in
 // the swizzle of a D-byte row, or (MXFP4 cache) the codes' exact bf16 values,
 // two 64-channel atoms [128][128 B], channels in the converters' order for K.
 // (In the prefix CTAs themselves this took 14500 cycles, 4 passes of 64 rows,
@@ -135,8 +215,9 @@ struct QueryParams {
     const uint16_t* q;
     int64_t qs0, qs1, qs2, qs3;
     int q_vec, n_rows, rows_pad, R, G;
-    uint8_t* img;
-    float* scale;
+    uint8_t* codes;                          // [Hk][rows_pad][D]
+    uint8_t* img;                            // null where no prefix_kernel reads it
+    float* scale;                            // [Hk][rows_pad]
 };
 
 template <int D, bool MX>
@@ -206,6 +287,9 @@ __global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
             w4[e] = amax != 0.0f ? (lo16 | (hi16 << 16)) : 0u;
         }
         const int chunk = (D / 64) * qq + c;
+        *reinterpret_cast<uint4*>(p.codes + ((size_t)hk * p.rows_pad + n) * D + 16 * chunk) =
+            make_uint4(w4[0], w4[1], w4[2], w4[3]);
+        if (p.img == nullptr) continue;
         if constexpr (MX) {
             // pair m of eight channels = (channel m, channel m + 4)
 #pragma unroll
@@ -227,7 +311,7 @@ __global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
 //   warps 0-7   softmax, two groups of four; thread = one query row (TMEM lane)
 //               and all 128 keys of a unit, so the row statistics need no
 //               shuffles;
-//   warps 8-11  V converters: e4m3 -> exact bf16 (MXFP4: K and V);
+//   warps 8-11  V converters: e4m3 -> exact fp16 (MXFP4: K and V -> bf16);
 //   warp 12     K/V producer (one TMA box per page), warps 13 and 15 MMA
 //               issuers of groups 0 and 1, warp 14 scale producer.
 // A unit is one 128-row x 64-key block of S: half h of a key tile, for group g.
@@ -237,23 +321,23 @@ __global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
 // same rows, group g takes the tiles of parity g, the units of tile i are
 // w = 2 i + h, and the groups' (m, l, O) are combined at the end.
 // Per unit: S = Q8 K8^T (TMEM, fp32, M = 128, N = 64) -> y = S k_scale -> row
-// max -> p = 2^(y c - m) -> P = bf16(p v_scale), written over S's own columns
+// max -> p = 2^(y c - m) -> P = fp16(p v_scale 2^-e) (MXFP4: bf16(p)), over S's own columns
 // as the A operand (in TMEM) of O += P V. S buffer [g][h] is used by every
 // fourth unit, so a group computes on one half while the products of the
 // other run: PV(w), then QK(w + 3) once PV(w - 1), which read P from that
 // buffer, has completed. (One 128-key unit a group in flight, its softmax
 // waiting for both products: 1800 of 5500 cycles a unit spent waiting, and 128
 // logits a thread spilled; 120 us against 62 us for 4096 rows x 32768 keys.)
-// The running max is only raised when a row's new maximum exceeds it by more
-// than 8 (base 2): p then stays below 2^8, which fp32 sums and bf16 weights
-// hold as exactly as values below one, and most tiles leave O alone.
 constexpr int kScStages = 8;                 // scale ring
+constexpr int kMinTiles = 2;                 // key tiles a CTA has in flight
 constexpr int kThreads = 512;
 constexpr int kConvWarp0 = 8, kTmaWarp = 12, kMmaWarp0 = 13, kScaleWarp = 14, kMmaWarp1 = 15;
 // 256 x 168 + 128 x 96 + 128 x 80 <= 512 x 128 registers, the launch's own
 constexpr int kRegsSoft = 168, kRegsConv = 96, kRegsProd = 80;
 static_assert(256 * kRegsSoft + 128 * kRegsConv + 128 * kRegsProd <= kThreads * 128, "register split");
-constexpr float kLazyMax = 8.0f;
+// A row's first maximum further below its starting point than this is taken as
+// the running max before any weight is computed (p would lose bits, or vanish).
+constexpr float kFarMax = 60.0f;
 // one pair of exponentials in 2 kPolyEvery goes to the FMA pipe
 constexpr int kPolyEvery = 4;
 
@@ -293,8 +377,8 @@ struct SmP {
     static constexpr int kVbBuf = kKeys * 2 * D;
     static constexpr int kScale = kVb + 2 * kVbBuf;                  // [slot][k | v][128] fp32
     static constexpr int kScSlot = MX ? 0 : 2 * kKeys;
-    static constexpr int kMeta = kScale + kScStages * kScSlot * 4;   // [slot] bad-page mask
-    static constexpr int kSpan = kMeta + kScStages * 4;              // [8 warps] lowest, highest key any row sees
+    static constexpr int kMeta = kScale + kScStages * kScSlot * 4;   // [slot] bad-page mask; exponent of the value scales
+    static constexpr int kSpan = kMeta + 2 * kScStages * 4;              // [8 warps] lowest, highest key any row sees
     static constexpr int kBar = kSpan + 2 * 8 * 4;
     static constexpr int kKvFull = 0, kKvEmpty = kKvFull + kStages, kSFull = kKvEmpty + kStages, kPReady = kSFull + 4,
                          kPvDone = kPReady + 4, kVReady = kPvDone + 4, kVFree = kVReady + 2, kFinal = kVFree + 2,
@@ -381,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= Sm::kKvEmpty && i < Sm::kKvEmpty + kStages) cnt = MX ? 4 : RG + 4; // (QK commits +) converters
             if (i >= Sm::kPReady && i < Sm::kPReady + 4) cnt = 4;                      // softmax group
             if (i >= Sm::kVReady && i < Sm::kVReady + 2) cnt = 4;                      // converters
-            if (i >= Sm::kScFull && i < Sm::kScFull + kScStages) cnt = 1 + 32;
+            if (i >= Sm::kScFull && i < Sm::kScFull + kScStages) cnt = 32;
             if (i >= Sm::kScEmpty && i < Sm::kScEmpty + kScStages) cnt = 4 * RG;       // the groups that read the tile
             if (i >= Sm::kKbReady && i < Sm::kKbReady + 2) cnt = 4;
             if (i >= Sm::kVFree && i < Sm::kVFree + 2) cnt = RG;                       // the groups' PV commits
@@ -443,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // key tiles [t0, t0 + n_all) that some row of the CTA sees; this split's share
     const int t0 = hi >= 0 ? lo / kKeys : 0;
     const int n_all = hi >= 0 ? hi / kKeys + 1 - t0 : 0;
-    const int nsp = shared_splits(n_all, p.np);
+    const int nsp = used_splits(n_all, p.np, kMinTiles);
     const int tb = t0 + (int)((int64_t)min(split, nsp) * n_all / nsp);
     const int nt = t0 + (int)((int64_t)min(split + 1, nsp) * n_all / nsp) - tb;
     const int ppt = kKeys / p.page;
@@ -458,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool kv = warp == kTmaWarp;
         const float ks_t = !MX && !kv && p.per_tensor ? __ldg(p.ksc) : 1.0f;
         const float vs_t = !MX && !kv && p.per_tensor ? __ldg(p.vsc) : 1.0f;
-        int chunk = -1, phys = 0, issued = 0;
-        bool bad = false;
+        int chunk = -1, phys = 0, issued = 0, vexp = kNoExp;
+        bool bad = false, found = false;
         if (kv && lane == 0 && nt > 0) {
             mbar_arrive_expect_tx(&bars[Sm::kQReady], kRowsCta * Sm::kQRow);
             bulk_load(sm + Sm::kQ, p.q_img + (size_t)blockIdx.y * kRowsCta * Sm::kQRow, kRowsCta * Sm::kQRow,
@@ -476,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 chunk = (i * ppt) / 32;
                 const int lp = tb * ppt + 32 * chunk + lane;
                 phys = 0;
-                bad = false;
+                bad = found = false;
                 if (lp < (tb + nt) * ppt && lp * p.page < L) {
                     const int pg = __ldg(p.ptab + lp);
                     if (pg < 0 || pg >= p.num_pages) {
@@ -484,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (kv) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
                     } else {
                         phys = pg;
+                        found = true;
                     }
                 }
             }
@@ -494,7 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(&bars[Sm::kKvFull + s], 2 * (Sm::kKStage + Sm::kSfStage));
                 __syncwarp();
                 if (mine) {
-                    const int z = phys * p.Hk + hk, q = lane - slot0;
+                    // FP8: a page without a key below L, or off the cache, is read
+                    // as zeros (a coordinate off the map): what its stand-in holds
+                    // could be NaN codes, which a weight of zero does not cancel
+                    const int z = MX || found ? phys * p.Hk + hk : -1, q = lane - slot0;
                     constexpr int kRowB = Sm::kKStage / kKeys;
                     tma_load_3d(sm + Sm::kK + s * Sm::kKStage + q * p.page * kRowB, &tmK, &bars[Sm::kKvFull + s], 0, 0, z);
                     tma_load_3d(sm + Sm::kV + s * Sm::kKStage + q * p.page * kRowB, &tmV, &bars[Sm::kKvFull + s], 0, 0, z);
@@ -509,28 +597,45 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 const unsigned badm = __ballot_sync(0xffffffffu, mine && bad) >> slot0;
-                if (lane == 0) {
-                    meta[c] = static_cast<int>(badm);
-                    mbar_arrive(&bars[Sm::kScFull + c]);
-                }
+                if (lane == 0) meta[c] = static_cast<int>(badm);
                 if constexpr (MX) {
                     mbar_arrive(&bars[Sm::kScFull + c]);
                 } else {
-                    float* dst = scl + c * Sm::kScSlot + 4 * lane;       // keys 4 lane .. 4 lane + 3
+                    // keys 4 lane .. 4 lane + 3: k_scale, and v_scale relative to
+                    // 2^vexp, zero where the slot holds no key of the prefix
+                    float ks[4], vs[4];
                     if (p.per_tensor) {
-                        *reinterpret_cast<float4*>(dst) = make_float4(ks_t, ks_t, ks_t, ks_t);
-                        *reinterpret_cast<float4*>(dst + kKeys) = make_float4(vs_t, vs_t, vs_t, vs_t);
-                        mbar_arrive(&bars[Sm::kScFull + c]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            ks[e] = ks_t;
+                            vs[e] = vs_t;
+                        }
                     } else {
                         const int pq = __shfl_sync(0xffffffffu, phys, slot0 + 4 * lane / p.page);
                         const int64_t src = ((int64_t)pq * p.Hk + hk) * p.page + (4 * lane) % p.page;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            cp_async_4(dst + e, p.ksc + src + e);
-                            cp_async_4(dst + kKeys + e, p.vsc + src + e);
+                            ks[e] = __ldg(p.ksc + src + e);
+                            vs[e] = __ldg(p.vsc + src + e);
                         }
-                        cp_async_mbar_arrive(&bars[Sm::kScFull + c]);
                     }
+                    const int key = (tb + i) * kKeys + 4 * lane;
+                    const bool off_page = (badm >> (4 * lane / p.page)) & 1;
+                    float vmax = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (key + e < lo || key + e > hi || off_page) vs[e] = 0.0f;
+                        vmax = fmaxf(vmax, vs[e]);
+                    }
+                    // (a scale is not negative: its bits order like its value)
+                    vexp = scale_exp(vexp, __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax))));
+                    const float f = vexp == kNoExp ? 0.0f : pow2i(-vexp);
+                    float* dst = scl + c * Sm::kScSlot + 4 * lane;
+                    *reinterpret_cast<float4*>(dst) = make_float4(ks[0], ks[1], ks[2], ks[3]);
+                    *reinterpret_cast<float4*>(dst + kKeys) =
+                        make_float4(vs[0] * f, vs[1] * f, vs[2] * f, vs[3] * f);
+                    if (lane == 0) meta[kScStages + c] = vexp;
+                    mbar_arrive(&bars[Sm::kScFull + c]);
                 }
             }
             issued = i + 1;
@@ -540,9 +645,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (nt > 0) mbar_wait_drain(&bars[Sm::kQReady], 0);
             for (int i = max(0, issued - kStages); i < issued; ++i)
                 mbar_wait_drain(&bars[Sm::kKvFull + i % kStages], (i / kStages) & 1);
-        } else {
-            for (int i = max(0, issued - kScStages); i < issued; ++i)
-                mbar_wait_drain(&bars[Sm::kScFull + i % kScStages], (i / kScStages) & 1);
         }
       } else {
         // ------------------------------------------------------------ MMA issuers
@@ -555,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int mt = RG == 2 ? nt : (nt - gu + 1) / 2;         // the group's tiles: j -> RG == 2 ? j : 2 j + gu
         if (mt > 0) {
             constexpr uint32_t kIdescQK = umma_idesc(1, MX ? 1 : 0, 128, 64);
-            const uint32_t idesc_pv = umma_idesc(1, 1, 128, D) | (p.v_trans ? 0u : 1u << 16);   // V: B MN-major
+            const uint32_t idesc_pv = umma_idesc(1, MX ? 1 : 0, 128, D) | (p.v_trans ? 0u : 1u << 16);   // bf16 | fp16; V: B MN-major
             const uint64_t qd = umma_desc_kmajor(smem_u32(sm + Sm::kQ), MX ? 128 : D) +
                                 (RG == 2 ? gu : 0) * ((128 * Sm::kQRow) >> 4);
             const uint64_t kd0 = MX ? umma_desc_kmajor(smem_u32(sm + Sm::kKb), 128)
@@ -649,13 +751,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       reg_alloc<kRegsSoft>();
         // ------------------------------------------------------------ softmax
         // base-2 logit = (S k_scale) cq; cq >= FLT_MIN keeps a masked -inf
-        const float cq = fmaxf(rv ? __ldg(p.q_scale + (size_t)blockIdx.y * kRowsCta + r) * p.logit_scale_log2 : 0.0f, FLT_MIN);
+        const float cq = fmaxf(rv ? __ldcg(p.q_scale + (size_t)blockIdx.y * kRowsCta + r) * p.logit_scale_log2 : 0.0f, FLT_MIN);
         const uint64_t cq2 = f2_pack(cq, cq);
         const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const uint32_t to = trow + kOCol + 128 * g;
         const bool idle = __all_sync(0xffffffffu, !rv);      // 32 rows of padding: the warp only keeps time
-        float m_run = -INFINITY;
+        // A row starts from m = 0, which holds for its first maximum too unless
+        // that is far off; l = 0 says that it has seen no key.
+        float m_run = 0.0f;
         uint64_t l2 = f2_pack(0.0f, 0.0f);
+        int vexp = kNoExp;                           // FP8: O is in units of 2^vexp
         bool ok = true;
         const int my_units = RG == 2 ? 2 * nt : 2 * ((nt - g + 1) / 2);
         for (int k = 0; k < my_units; ++k) {
@@ -704,9 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     f2_unpack(p01, p0, p1);
                     f2_unpack(p23, p2, p3);
-                    const __nv_bfloat162 b01 = __floats2bfloat162_rn(p0, p1), b23 = __floats2bfloat162_rn(p2, p3);
-                    w[2 * q] = *reinterpret_cast<const uint32_t*>(&b01);
-                    w[2 * q + 1] = *reinterpret_cast<const uint32_t*>(&b23);
+                    w[2 * q] = MX ? bf16x2(p0, p1) : f16x2(p0, p1);
+                    w[2 * q + 1] = MX ? bf16x2(p2, p3) : f16x2(p2, p3);
                 };
                 uint32_t x0[32], x1[32];
                 tmem_ld32(ts, x0);
@@ -718,10 +822,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // running one while the unit's own is still being found: one
                 // pass in which loads, FMA and MUFU overlap. Where the unit
                 // turns out to need more, nothing of the pass is kept.
-                bool slow = k == 0 || !__all_sync(0xffffffffu, !rv || (key0 >= key_lo && key0 + 63 <= key_hi && badm == 0));
+                const int ve = MX ? 0 : meta[kScStages + c];
+                if (vexp == kNoExp) vexp = ve;               // (no key before: O holds zeros)
+                bool slow = ve != vexp || !__all_sync(0xffffffffu, !rv || (key0 >= key_lo && key0 + 63 <= key_hi && badm == 0));
                 if (!slow) {
-                    const float sub = m_run == -INFINITY ? 0.0f : m_run;
-                    const uint64_t nsub2 = f2_pack(-sub, -sub);
+                    const uint64_t nsub2 = f2_pack(-m_run, -m_run);
                     uint64_t l = l2;
                     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     uint32_t w[2][16];
@@ -740,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * cq;
-                    slow = __any_sync(0xffffffffu, rv && mx > m_run + kLazyMax);
+                    slow = __any_sync(0xffffffffu, rv && (mx > m_run + kLazyMax || (l2 == 0 && mx < m_run - kFarMax)));
                     if (!slow) {
                         l2 = l;
                         tmem_st16(ts, w[0]);
@@ -774,10 +879,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     mx = mx == -INFINITY ? -INFINITY : mx * cq;
                     float alpha = 1.0f;
-                    if (mx > m_run + kLazyMax) {              // (a first key too: m_run = -inf)
-                        alpha = m_run == -INFINITY ? 1.0f : ex2_approx(m_run - mx);
+                    if (l2 == 0) {
+                        if (mx > -INFINITY) m_run = mx;       // its first key (O is zero)
+                    } else if (mx > m_run + kLazyMax) {
+                        alpha = ex2_approx(m_run - mx);
                         l2 = f2_mul(l2, f2_pack(alpha, alpha));
                         m_run = mx;
+                    }
+                    if (ve != vexp) {
+                        alpha *= pow2i(vexp - ve);
+                        vexp = ve;
                     }
                     // O of the rows whose maximum was raised, once the group's
                     // last PV has completed
@@ -796,8 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tmem_st16(to + 16 * hf, o);
                         }
                     }
-                    const float sub = m_run == -INFINITY ? 0.0f : m_run;
-                    const uint64_t nsub2 = f2_pack(-sub, -sub);
+                    const uint64_t nsub2 = f2_pack(-m_run, -m_run);
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
                         uint32_t w[16];
@@ -823,10 +933,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float l0, l1;
         f2_unpack(l2, l0, l1);
         float l = l0 + l1;
-        if (!ok || my_units == 0 || m_run == -INFINITY) {
+        if (!ok || l == 0.0f) {                      // (no key seen)
             m_run = -INFINITY;
             l = 0.0f;
         }
+        const float unit = MX || vexp == kNoExp ? 1.0f : pow2i(vexp);
         tc_fence_after();
         // channel of TMEM column j (MX: the order of the converted V rows)
         auto chan = [](int j) { return MX ? (j & ~7) + ((j >> 1) & 3) + 4 * (j & 1) : j; };
@@ -840,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(to + 32 * hf, o);
                     tmem_wait_ld(o);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) po[chan(32 * hf + j) * kRowsCta] = __uint_as_float(o[j]);
+                    for (int j = 0; j < 32; ++j) po[chan(32 * hf + j) * kRowsCta] = __uint_as_float(o[j]) * unit;
                 }
             }
             tc_fence_before();
@@ -860,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_ld32(to + give + 32 * hf, o);
                     tmem_wait_ld(o);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) xo[(give + 32 * hf + j) * 128 + r] = __uint_as_float(o[j]);
+                    for (int j = 0; j < 32; ++j) xo[(give + 32 * hf + j) * 128 + r] = __uint_as_float(o[j]) * unit;
                 }
             }
             named_sync(1, 256);
@@ -879,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 32; ++j) {
                         const int col = keep + 32 * hf + j;
                         // (a group without a key in the row has no O)
-                        float y = m_run == -INFINITY ? 0.0f : wa * __uint_as_float(o[j]);
+                        float y = m_run == -INFINITY ? 0.0f : wa * unit * __uint_as_float(o[j]);
                         if (other.x != -INFINITY) y = fmaf(wb, xo[col * 128 + r], y);
                         po[chan(col) * 128] = y;
                     }
@@ -935,7 +1046,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 // 16-byte chunk c of the code row (V: 16 channels of a key;
-                // V^T: 16 keys of a channel) -> two chunks of the bf16 row
+                // V^T: 16 keys of a channel) -> two chunks of the fp16 row;
+                // slots behind the prefix's end count as zeros
+                const int left = L - (tb + i) * kKeys;           // keys of the tile below L
                 auto convert = [&](auto width_c, int atom_b) {
                     constexpr int kWidth = decltype(width_c)::value;
                     const uint8_t* vrow = sm + Sm::kV + s * Sm::kKStage + row * kWidth;
@@ -943,16 +1056,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kWidth / 16; ++c)
                         u[c] = *reinterpret_cast<const uint4*>(vrow + (e4m3_chunk<kWidth>(c, row) << 4));
+                    if (left < kKeys) {
+#pragma unroll
+                        for (int c = 0; c < kWidth / 16; ++c) {
+                            const int n = p.v_trans ? left - 16 * c : (row < left ? 16 : 0);
+                            u[c].x &= low_bytes(n);
+                            u[c].y &= low_bytes(n - 4);
+                            u[c].z &= low_bytes(n - 8);
+                            u[c].w &= low_bytes(n - 12);
+                        }
+                    }
 #pragma unroll
                     for (int c = 0; c < kWidth / 16; ++c) {
                         uint8_t* at = dst + (c >> 2) * atom_b;
                         const int ch = 2 * (c & 3);
                         *reinterpret_cast<uint4*>(at + ((ch ^ (row & 7)) << 4)) =
-                            make_uint4(e4m3x2_to_bf16x2(u[c].x, 0x1404u), e4m3x2_to_bf16x2(u[c].x, 0x3424u),
-                                       e4m3x2_to_bf16x2(u[c].y, 0x1404u), e4m3x2_to_bf16x2(u[c].y, 0x3424u));
+                            make_uint4(e4m3_lo_to_f16x2(u[c].x), e4m3_hi_to_f16x2(u[c].x), e4m3_lo_to_f16x2(u[c].y),
+                                       e4m3_hi_to_f16x2(u[c].y));
                         *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (row & 7)) << 4)) =
-                            make_uint4(e4m3x2_to_bf16x2(u[c].z, 0x1404u), e4m3x2_to_bf16x2(u[c].z, 0x3424u),
-                                       e4m3x2_to_bf16x2(u[c].w, 0x1404u), e4m3x2_to_bf16x2(u[c].w, 0x3424u));
+                            make_uint4(e4m3_lo_to_f16x2(u[c].z), e4m3_hi_to_f16x2(u[c].z), e4m3_lo_to_f16x2(u[c].w),
+                                       e4m3_hi_to_f16x2(u[c].w));
                     }
                 };
                 if (p.v_trans) {
@@ -981,57 +1104,569 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// -------------------------------------------------------------- few rows
+
+// Up to 64 query rows against a run of keys: a sequence's own rows against its
+// own keys [L, ctx), and, where the whole batch has no more rows than that,
+// all rows against the prefix. With 16 rows a key costs 4 D FLOPs a byte of
+// cache, far from what a tensor pipe is bound by; what counts is latency and
+// bytes in flight. So no TMEM, no shared-memory operands and no roles: a warp
+// takes 16 rows and 64 keys at a time straight from global memory into
+// mma fragments (FP8: QK on the e4m3 codes, PV on fp16; MXFP4: both on bf16),
+// and three CTAs of four independent warps share an SM. (decode.cu's kernel, one CTA an SM, took 27 us for 256 sequences of at
+// most 512 own keys where this takes 8.)
+// Fragments. The order of the summed index is free as long as both operands
+// have the same, and so is the order of output columns; with thread (g, c) =
+// (lane / 4, lane % 4):
+//   S = Q K^T  summed index: thread c holds the run d = c D / 4 .. of its key
+//              (16 or 32 contiguous bytes), 4 elements a step; column n of
+//              n-tile j is key 16 (n / 2) + 2 j + n % 2 of the block, so that
+//              thread c's columns are the 16 consecutive keys 16 c ..
+//   O = P V    step s of 16 keys = n-tiles 2 s and 2 s + 1, whose S registers
+//              are P's A operand; thread (g, c) holds V of keys 16 c + 4 s ..
+//              + 3 (V^T: four bytes of a 16-byte run) and channels D g / 8 ..,
+//              one per n-tile, converted exactly in registers.
+constexpr int kBlk = 64;                     // keys a warp takes at a time
+constexpr int kRowsWarps = 4;
+
+struct RowsParams {
+    const uint8_t* q8;                       // [Hk][rows_pad][D] e4m3 codes
+    const float* q_scale;                    // [Hk][rows_pad]
+    const uint8_t* kc;
+    const uint8_t* vc;
+    const float* ksc;
+    const float* vsc;
+    const uint8_t* ksf;
+    const uint8_t* vsf;
+    int per_tensor, sc_vec;                  // scales' base 16-byte aligned
+    const int32_t* ptab;                     // [B, max_pages]
+    const int32_t* prefix;
+    const int32_t* plen;
+    const int32_t* ctx;
+    int B, T, Hk, G, R, n_rows, rows_pad, lg_page, max_pages, cap_prefix, num_pages, window;
+    int np, ns;                              // splits of the prefix part (0: not here), of a sequence's own
+    float logit_scale_log2;
+    float2* pre_stat;                        // [Hk][np][64]
+    float* pre_o;                            // [Hk][np][D][64]
+    float2* own_stat;                        // [B Hk][ns][64]
+    float* own_o;
+    int late_wait;                           // launched behind prefix_kernel, of which it reads nothing
+};
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_16832_e4m3(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+template <int D, bool MX, bool VT>
+__global__ void __launch_bounds__(32 * kRowsWarps, 3) rows_kernel(const RowsParams p) {
+    constexpr int kSteps = MX ? D / 16 : D / 32; // QK steps
+    constexpr int kNt = D / 8;                   // n-tiles of O = channels a thread has of a V row
+    constexpr int kKB = MX ? D / 8 : D / 4;      // bytes of a key's row a thread holds
+    constexpr int kRowB = MX ? D / 2 : D;
+    constexpr int kVB = MX ? D / 16 : D / 8;     // bytes of a value's row
+    constexpr int kPitch = 17;                   // rows of a staged O
+    __shared__ __align__(16) float o_s[kRowsWarps][D * kPitch];
+    __shared__ float2 stat_s[kRowsWarps][16];
+    __shared__ int lo_s, hi_s;
+    uint4* qf = reinterpret_cast<uint4*>(&o_s[0][0]);         // [m-tile][step][lane] (until O is staged)
+    static_assert(!MX || 4 * kSteps * 32 * 16 <= sizeof(o_s), "query fragments");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    if (!p.late_wait) pdl_wait();
+    pdl_launch_dependents();
+
+    const bool pre = (int)blockIdx.x < p.np * p.Hk;
+    const int bi = pre ? blockIdx.x : blockIdx.x - p.np * p.Hk;
+    const int nsplit = pre ? p.np : p.ns;
+    const int item = bi / nsplit, split = bi % nsplit;
+    const int hk = pre ? item : item % p.Hk, b = pre ? 0 : item / p.Hk;
+    const int rows = pre ? p.n_rows : p.R;
+    const int n0 = b * p.R;                                   // first row (pre: b = 0)
+    int L = *p.plen;
+    if (L < 0 || L > p.cap_prefix) {
+        if (tid == 0 && split == 0) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
+        L = max(0, min(L, p.cap_prefix));
+    }
+    const int cap = p.max_pages << p.lg_page;
+    // keys that row r sees of this part
+    auto see = [&](int r, int& klo, int& khi) {
+        klo = INT32_MAX;
+        khi = -1;
+        if (r < rows) {
+            const int n = n0 + r;
+            const int ctx = max(0, min(__ldg(p.ctx + n / p.R), cap));
+            const int pq = ctx - p.T + (n % p.R) / p.G;
+            const int a = max(pre ? 0 : L, pq - p.window + 1), e = pre ? min(pq, L - 1) : pq;
+            if (e >= a) {
+                klo = a;
+                khi = e;
+            }
+        }
+    };
+    if (!pre && tid == 0 && split == 0) {
+        const int ctx = __ldg(p.ctx + b);
+        if (ctx < 0 || ctx > cap) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
+    }
+    // warps: m-tile (16 rows) x key slice
+    const int mts = (rows + 15) >> 4, slices = kRowsWarps / mts;
+    const int mt = warp / slices, slice = warp % slices;
+    const bool live = mt < mts;
+    int klo[2], khi[2];
+    see(16 * mt + g, klo[0], khi[0]);
+    see(16 * mt + g + 8, klo[1], khi[1]);
+    if (tid == 0) {
+        lo_s = INT32_MAX;
+        hi_s = -1;
+    }
+    __syncthreads();
+    {
+        const int lo = __reduce_min_sync(0xffffffffu, live ? min(klo[0], klo[1]) : INT32_MAX);
+        const int hi = __reduce_max_sync(0xffffffffu, live ? max(khi[0], khi[1]) : -1);
+        if (lane == 0) {
+            atomicMin(&lo_s, lo);
+            atomicMax(&hi_s, hi);
+        }
+    }
+    // the query codes as A fragments, thread (g, c) holding the run c D / 4 ..
+    // of rows g and g + 8: e4m3 as they are; for an MXFP4 cache their exact
+    // bf16 values, pairs (m, m + 4) of eight channels as e2m1_block_to_bf16
+    // orders K's, in shared memory
+    uint4 qa[MX ? 1 : kSteps];
+    {
+        const uint8_t* src = p.q8 + ((size_t)hk * p.rows_pad + n0 + 16 * mt + g) * D + c * (D / 4);
+        uint4 u[2][D / 64];
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int k = 0; k < D / 64; ++k)
+                u[r][k] = live && 16 * mt + g + 8 * r < rows
+                              ? __ldcg(reinterpret_cast<const uint4*>(src + 8 * r * D) + k)
+                              : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t* w0 = reinterpret_cast<const uint32_t*>(u[0]);
+        const uint32_t* w1 = reinterpret_cast<const uint32_t*>(u[1]);
+#pragma unroll
+        for (int st = 0; st < kSteps; ++st) {
+            if constexpr (MX) {
+                const int k = st & ~1;
+                uint4 a;
+                if ((st & 1) == 0)
+                    a = make_uint4(e4m3_pick_to_bf16x2<0>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<0>(w1[k], w1[k + 1]),
+                                   e4m3_pick_to_bf16x2<1>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<1>(w1[k], w1[k + 1]));
+                else
+                    a = make_uint4(e4m3_pick_to_bf16x2<2>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<2>(w1[k], w1[k + 1]),
+                                   e4m3_pick_to_bf16x2<3>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<3>(w1[k], w1[k + 1]));
+                if (live && slice == 0) qf[(mt * kSteps + st) * 32 + lane] = a;
+            } else {
+                qa[st] = make_uint4(w0[2 * st], w1[2 * st], w0[2 * st + 1], w1[2 * st + 1]);
+            }
+        }
+    }
+    float cq[2] = {FLT_MIN, FLT_MIN};            // base-2 logit = (S k_scale) cq; > 0 keeps a masked -inf
+    if (live) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+            if (16 * mt + g + 8 * r < rows)
+                cq[r] = fmaxf(__ldcg(p.q_scale + (size_t)hk * p.rows_pad + n0 + 16 * mt + g + 8 * r) * p.logit_scale_log2,
+                              FLT_MIN);
+    }
+    const float ks_t = !MX && p.per_tensor ? __ldg(p.ksc) : 1.0f, vs_t = !MX && p.per_tensor ? __ldg(p.vsc) : 1.0f;
+    __syncthreads();
+    const int lo = lo_s, hi = hi_s;
+    const int blk0 = hi >= 0 ? lo / kBlk : 0, n_all = hi >= 0 ? hi / kBlk + 1 - blk0 : 0;
+    const int nsp = used_splits(n_all, nsplit, slices);
+    const int first = blk0 + (int)((int64_t)min(split, nsp) * n_all / nsp);
+    const int last = blk0 + (int)((int64_t)min(split + 1, nsp) * n_all / nsp);
+
+    const int32_t* tab = pre ? p.prefix : p.ptab + (int64_t)b * p.max_pages;
+    const int end_tok = pre ? L : hi + 1;                     // pages from here on hold no key of the part
+    const int lgp = min(p.lg_page, 6);                        // keys of one page inside a block (log2)
+    float O[kNt][4];
+#pragma unroll
+    for (int t = 0; t < kNt; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[t][e] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    int vexp = kNoExp;                                        // FP8: O is in units of 2^vexp
+    for (int blk = first + slice; live && blk < last; blk += slices) {
+        const int k0 = blk * kBlk;
+        // pages of the block: lane i holds page i
+        int phys = 0;
+        bool bad = false;
+        {
+            const int lp = (k0 >> p.lg_page) + lane;
+            if (lane < (kBlk >> lgp) && (lp << p.lg_page) < end_tok && ((lp + 1) << p.lg_page) > lo) {
+                const int pg = __ldg(tab + lp);
+                bad = pg < 0 || pg >= p.num_pages;
+                if (bad) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
+                else phys = pg;
+            }
+        }
+        const unsigned badm = __ballot_sync(0xffffffffu, bad);
+        const int in0 = k0 & ((1 << p.lg_page) - 1);          // block's offset in a larger page
+        // (page, head, offset) index of key o of the block
+        auto token = [&](int o) -> int64_t {
+            const int pg = __shfl_sync(0xffffffffu, phys, o >> lgp);
+            return (((int64_t)pg * p.Hk + hk) << p.lg_page) + in0 + (o & ((1 << lgp) - 1));
+        };
+        // ---- S = Q K^T
+        float S[8][4];
+#pragma unroll
+        for (int jh = 0; jh < 2; ++jh) {
+            uint4 kr[4][MX ? 1 : D / 64];
+            uint32_t ke[4];
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                const int64_t tk = token(16 * (g >> 1) + 2 * (4 * jh + jj) + (g & 1));
+                const uint4* src = reinterpret_cast<const uint4*>(p.kc + tk * kRowB + c * kKB);
+#pragma unroll
+                for (int k = 0; k < (MX ? 1 : D / 64); ++k) kr[jj][k] = __ldg(src + k);
+                ke[jj] = MX ? __ldg(p.ksf + tk * 4 + c) : 0u;
+            }
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) S[4 * jh + jj][e] = 0.0f;
+            if constexpr (MX) {
+                uint32_t kb[4][16];
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) e2m1_block_to_bf16(kr[jj][0], ke[jj], kb[jj]);
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st) {
+                    const uint4 a = qf[(mt * kSteps + st) * 32 + lane];
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj) mma_16816(S[4 * jh + jj], a, kb[jj][2 * st], kb[jj][2 * st + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+                    for (int jj = 0; jj < 4; ++jj) {
+                        const uint32_t* w = reinterpret_cast<const uint32_t*>(kr[jj]);
+                        mma_16832_e4m3(S[4 * jh + jj], qa[st], w[2 * st], w[2 * st + 1]);
+                    }
+            }
+        }
+        // ---- scales of keys 16 c .., masks, maxima
+        float vs[16];
+        if constexpr (!MX) {
+            const int64_t tk = token(16 * c);                 // (16 consecutive keys are in one page)
+            if (p.per_tensor) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) vs[k] = vs_t;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) S[j][e] *= ks_t;
+            } else if (p.sc_vec) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 s = __ldg(reinterpret_cast<const float4*>(p.ksc + tk) + k);
+                    const float4 v = __ldg(reinterpret_cast<const float4*>(p.vsc + tk) + k);
+                    S[2 * k][0] *= s.x;
+                    S[2 * k][1] *= s.y;
+                    S[2 * k][2] *= s.x;
+                    S[2 * k][3] *= s.y;
+                    S[2 * k + 1][0] *= s.z;
+                    S[2 * k + 1][1] *= s.w;
+                    S[2 * k + 1][2] *= s.z;
+                    S[2 * k + 1][3] *= s.w;
+                    vs[4 * k] = v.x;
+                    vs[4 * k + 1] = v.y;
+                    vs[4 * k + 2] = v.z;
+                    vs[4 * k + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float s = __ldg(p.ksc + tk + k);
+                    vs[k] = __ldg(p.vsc + tk + k);
+                    S[k >> 1][k & 1] *= s;
+                    S[k >> 1][2 + (k & 1)] *= s;
+                }
+            }
+        }
+        const bool bad_c = (badm >> ((16 * c) >> lgp)) & 1;
+        // of keys 16 c .. this thread's, no row sees those outside [va, ve]
+        const int va = lo - k0 - 16 * c, ve = bad_c ? -1 : hi - k0 - 16 * c;
+        const bool edge = !__all_sync(0xffffffffu, va <= 0 && ve >= 15);
+        if constexpr (!MX) {
+            // value scales relative to 2^vexp, zero where no row sees the key
+            if (edge) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (k < va || k > ve) vs[k] = 0.0f;
+            }
+            float vmax = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) vmax = fmax3(vmax, vs[k], vs[k + 1]);
+            vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
+            vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+            const int ne = scale_exp(vexp, vmax);
+            if (ne != vexp) {
+                if (vexp != kNoExp) {
+                    const float f = pow2i(vexp - ne);
+#pragma unroll
+                    for (int t = 0; t < kNt; ++t)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) O[t][x] *= f;
+                }
+                vexp = ne;
+            }
+            const float f = vexp == kNoExp ? 0.0f : pow2i(-vexp);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) vs[k] *= f;
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int a = klo[r] - k0 - 16 * c, e = khi[r] - k0 - 16 * c;    // key 16 c + k is seen for a <= k <= e
+            if (!__all_sync(0xffffffffu, a <= 0 && e >= 15 && !bad_c)) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (k < a || k > e || bad_c) S[k >> 1][2 * r + (k & 1)] = -INFINITY;
+            }
+            float mx = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) mx = fmax3(mx, S[k >> 1][2 * r], S[k >> 1][2 * r + 1]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            mx = mx == -INFINITY ? -INFINITY : mx * cq[r];
+            const bool raise = mx > m[r] + kLazyMax;          // (a first key too)
+            const float alpha = raise && m[r] != -INFINITY ? ex2_approx(m[r] - mx) : 1.0f;
+            if (raise) m[r] = mx;
+            if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+                l[r] *= alpha;
+#pragma unroll
+                for (int t = 0; t < kNt; ++t) {
+                    O[t][2 * r] *= alpha;
+                    O[t][2 * r + 1] *= alpha;
+                }
+            }
+            const float sub = m[r] == -INFINITY ? 0.0f : m[r];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const float x = ex2_approx(fmaf(S[k >> 1][2 * r + (k & 1)], cq[r], -sub));
+                l[r] += x;
+                S[k >> 1][2 * r + (k & 1)] = MX ? x : x * vs[k];
+            }
+        }
+        // ---- O += P V
+        if constexpr (VT) {
+            uint4 pa[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                pa[s] = make_uint4(f16x2(S[2 * s][0], S[2 * s][1]), f16x2(S[2 * s][2], S[2 * s][3]),
+                                   f16x2(S[2 * s + 1][0], S[2 * s + 1][1]), f16x2(S[2 * s + 1][2], S[2 * s + 1][3]));
+            const int pg = __shfl_sync(0xffffffffu, phys, 0);
+            const uint8_t* src = p.vc + (((int64_t)pg * p.Hk + hk) * D + kNt * g) * 128 + in0 + 16 * c;
+#pragma unroll
+            for (int t0 = 0; t0 < kNt; t0 += 4) {
+                uint4 u[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) u[t] = __ldg(reinterpret_cast<const uint4*>(src + (t0 + t) * 128));
+                if (edge) {                                   // (a NaN code times a weight of 0 is not 0)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        u[t].x &= low_bytes(ve + 1) & ~low_bytes(va);
+                        u[t].y &= low_bytes(ve - 3) & ~low_bytes(va - 4);
+                        u[t].z &= low_bytes(ve - 7) & ~low_bytes(va - 8);
+                        u[t].w &= low_bytes(ve - 11) & ~low_bytes(va - 12);
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    const uint32_t w[4] = {u[t].x, u[t].y, u[t].z, u[t].w};
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        mma_16816_f16(O[t0 + t], pa[s], e4m3_lo_to_f16x2(w[s]), e4m3_hi_to_f16x2(w[s]));
+                }
+            }
+        } else {
+            constexpr int kW = kVB / 4;                       // words of a value's run
+            uint32_t v[2][4][kW], vsf[2][4];
+            const int64_t tk = token(16 * c);
+            auto load_v = [&](int s) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint8_t* src = p.vc + (tk + 4 * s + k) * kRowB + g * kVB;
+                    if constexpr (kW == 4) {
+                        const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
+                        v[s & 1][k][0] = u.x;
+                        v[s & 1][k][1] = u.y;
+                        v[s & 1][k][kW - 2] = u.z;
+                        v[s & 1][k][kW - 1] = u.w;
+                    } else {
+                        const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
+                        v[s & 1][k][0] = u.x;
+                        v[s & 1][k][1] = u.y;
+                    }
+                    vsf[s & 1][k] = MX ? __ldg(p.vsf + (tk + 4 * s + k) * 4 + (g >> 1)) : 0u;
+                }
+            };
+            load_v(0);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (s < 3) load_v(s + 1);
+                auto pair = [](float x, float y) { return MX ? bf16x2(x, y) : f16x2(x, y); };
+                const uint4 a = make_uint4(pair(S[2 * s][0], S[2 * s][1]), pair(S[2 * s][2], S[2 * s][3]),
+                                           pair(S[2 * s + 1][0], S[2 * s + 1][1]),
+                                           pair(S[2 * s + 1][2], S[2 * s + 1][3]));
+                auto& w = v[s & 1];
+                if (!MX && edge) {                            // (a NaN code times a weight of 0 is not 0)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (4 * s + k < va || 4 * s + k > ve) {
+#pragma unroll
+                            for (int x = 0; x < kW; ++x) w[k][x] = 0u;
+                        }
+                }
+                if constexpr (MX) {
+                    // 16 channels of four keys: pairs (channel m, m + 4) of eight
+                    // first, then the same channel of two keys side by side
+                    uint32_t x[4][8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t E = min(vsf[s & 1][k], 252u);
+                        const uint32_t e1 = E <= 128u ? E + 126u : 253u;
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) e2m1x8_to_bf16(w[k][q], (e1 << 7) | (e1 << 23), x[k] + 4 * q);
+                        if (E > 128u) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) x[k][q] = bf16x2_mul(x[k][q], (E << 7) | (E << 23));
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) {
+                        const int q = 4 * (t >> 3) + (t & 3);
+                        const uint32_t sel = (t & 4) ? 0x7632u : 0x5410u;
+                        mma_16816(O[t], a, __byte_perm(x[0][q], x[1][q], sel), __byte_perm(x[2][q], x[3][q], sel));
+                    }
+                } else {
+                    // byte pairs (key 0, key 1) and (key 2, key 3) of two channels
+                    // at a time
+#pragma unroll
+                    for (int t = 0; t < kNt; t += 2) {
+                        const uint32_t sel = (t & 2) ? 0x7362u : 0x5140u;
+                        const uint32_t x = __byte_perm(w[0][t >> 2], w[1][t >> 2], sel);
+                        const uint32_t y = __byte_perm(w[2][t >> 2], w[3][t >> 2], sel);
+                        mma_16816_f16(O[t], a, e4m3_lo_to_f16x2(x), e4m3_lo_to_f16x2(y));
+                        mma_16816_f16(O[t + 1], a, e4m3_hi_to_f16x2(x), e4m3_hi_to_f16x2(y));
+                    }
+                }
+            }
+        }
+    }
+    // ---- the warp's (m, l, O), staged [channel][row]; the slices combined
+    __syncthreads();                                          // the query fragments are done with
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+        if (c == 0) stat_s[warp][g + 8 * r] = make_float2(m[r], l[r]);
+    }
+    float* os = o_s[warp];
+    const float unit = MX || vexp == kNoExp ? 1.0f : pow2i(vexp);
+#pragma unroll
+    for (int t = 0; t < kNt; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) os[(kNt * (2 * c + (e & 1)) + t) * kPitch + g + 8 * (e >> 1)] = O[t][e] * unit;
+    __syncthreads();
+    const size_t part = (size_t)item * nsplit + split;
+    float2* stat = (pre ? p.pre_stat : p.own_stat) + part * 64;
+    float* out = (pre ? p.pre_o : p.own_o) + part * D * 64;
+    for (int r = tid; r < rows; r += 32 * kRowsWarps) {
+        float M = -INFINITY, ls = 0.0f;
+        for (int s = 0; s < slices; ++s) M = fmaxf(M, stat_s[(r >> 4) * slices + s][r & 15].x);
+        for (int s = 0; s < slices; ++s) {
+            const float2 x = stat_s[(r >> 4) * slices + s][r & 15];
+            if (x.x != -INFINITY) ls = fmaf(ex2_approx(x.x - M), x.y, ls);
+        }
+        stat[r] = make_float2(M, ls);
+    }
+    // thread: row tid % 16 of an m-tile, channels tid / 16, + 8, ... (a part
+    // without keys has no O)
+    for (int t = 0; t < (first < last ? mts : 0); ++t) {
+        const int r = tid & 15;
+        if (16 * t + r >= rows) continue;
+        float wt[kRowsWarps], M = -INFINITY;
+        for (int s = 0; s < slices; ++s) M = fmaxf(M, stat_s[t * slices + s][r].x);
+#pragma unroll
+        for (int s = 0; s < kRowsWarps; ++s) {
+            const float ms = s < slices ? stat_s[t * slices + s][r].x : -INFINITY;
+            wt[s] = ms == -INFINITY ? 0.0f : ex2_approx(ms - M);
+        }
+        for (int d = tid >> 4; d < D; d += 2 * kRowsWarps) {
+            float y = 0.0f;
+#pragma unroll
+            for (int s = 0; s < kRowsWarps; ++s)
+                if (s < slices) y = fmaf(wt[s], o_s[t * slices + s][d * kPitch + r], y);
+            out[d * 64 + 16 * t + r] = y;
+        }
+    }
+    if (p.late_wait) pdl_wait();                              // this grid ends after the one before it
+}
+
 // ------------------------------------------------------------------ launch
 
-// Where the partials of the two parts lie in the workspace.
+// How a batch's work is cut, and where its pieces lie in the workspace.
 struct SharedPlan {
-    int pre_rows, n_rt, np, ns;              // rows a prefix CTA has, tiles of them, their splits; own splits
-    size_t pre_stat, pre_o, own_stat, own_o, q_img, q_scale, bytes;
+    int pre_rows, n_rt, np, ns;              // rows of a prefix CTA, tiles of them, their splits; a sequence's splits
+    int rows_pad;
+    size_t pre_stat, pre_o, own_stat, own_o, codes, img, q_scale, bytes;
 };
 
 SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
     SharedPlan w;
-    const int64_t rows = (int64_t)B * T * (H / Hk);
+    const int64_t rows = (int64_t)B * T * (H / Hk), sms = device_sms();
     w.pre_rows = rows <= kFewRows ? kFewRows : (rows <= 256 ? 128 : 256);
     w.n_rt = (int)ceil_div(rows, w.pre_rows);
-    const int sms = device_sms();
-    w.np = (int)std::max<int64_t>(1, sms / ((int64_t)w.n_rt * Hk));
-    w.ns = (int)std::max<int64_t>(1, std::min<int64_t>(16, sms / ((int64_t)B * Hk)));
+    // one CTA an SM for prefix_kernel, three for rows_kernel
+    const bool few = w.pre_rows == kFewRows;
+    w.np = (int)std::max<int64_t>(1, (few ? 2 * sms : sms) / ((int64_t)w.n_rt * Hk));
+    w.ns = (int)std::max<int64_t>(1, std::min<int64_t>(32, (few ? 1 : 3) * sms / ((int64_t)B * Hk)));
+    w.rows_pad = few ? (int)rows : w.n_rt * w.pre_rows;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t o = at;
+        at += (n + 255) & ~(size_t)255;
+        return o;
+    };
     const size_t pre = (size_t)w.n_rt * Hk * w.np * w.pre_rows, own = (size_t)B * Hk * w.ns * 64;
-    w.pre_stat = 0;
-    w.own_stat = w.pre_stat + pre * sizeof(float2);
-    w.pre_o = w.own_stat + own * sizeof(float2);
-    w.own_o = w.pre_o + pre * D * sizeof(float);
-    w.q_img = w.own_o + own * D * sizeof(float);
-    const size_t q_rows = w.pre_rows == kFewRows ? 0 : (size_t)Hk * w.n_rt * w.pre_rows;
-    w.q_scale = w.q_img + q_rows * 2 * D;                    // (bf16 images for an MXFP4 cache)
-    w.bytes = w.q_scale + q_rows * sizeof(float);
+    const size_t q_rows = (size_t)Hk * w.rows_pad;
+    w.pre_stat = take(pre * sizeof(float2));
+    w.own_stat = take(own * sizeof(float2));
+    w.pre_o = take(pre * D * sizeof(float));
+    w.own_o = take(own * D * sizeof(float));
+    w.codes = take(q_rows * D);
+    w.img = take(few ? 0 : q_rows * 2 * D);                  // (bf16 images for an MXFP4 cache)
+    w.q_scale = take(q_rows * sizeof(float));
+    w.bytes = at;
     return w;
 }
 
 template <int D, bool MX, int RG>
-cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, const SharedPart& part, cudaStream_t s) {
+cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, cudaStream_t s) {
     const DecodeArgs& a = sa.d;
     constexpr int kSmem = SmP<D, MX, RG>::kBytes + 1024;
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
-    QueryParams qp;
-    qp.q = static_cast<const uint16_t*>(a.q.ptr);
-    qp.qs0 = a.q.stride[0];
-    qp.qs1 = a.q.stride[1];
-    qp.qs2 = a.q.stride[2];
-    qp.qs3 = a.q.stride[3];
-    qp.q_vec = view_vec8(a.q) ? 1 : 0;
-    qp.G = a.H / a.Hk;
-    qp.R = a.T * qp.G;
-    qp.n_rows = a.B * qp.R;
-    qp.rows_pad = w.n_rt * w.pre_rows;
-    qp.img = ws + w.q_img;
-    qp.scale = reinterpret_cast<float*>(ws + w.q_scale);
-    cudaError_t e = launch_pdl(query_kernel<D, MX>, dim3((unsigned)ceil_div(qp.n_rows, 32), a.Hk), dim3(128), 0, s, qp);
-    if (e != cudaSuccess) return e;
     PrefixParams p = {};
-    p.q_img = qp.img;
-    p.q_scale = qp.scale;
+    p.q_img = ws + w.img;
+    p.q_scale = reinterpret_cast<const float*>(ws + w.q_scale);
     p.ksc = a.k_scale;
     p.vsc = a.v_scale;
     p.per_tensor = (a.kv_flags & 1) ? 1 : 0;
@@ -1051,12 +1686,12 @@ cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, const
     p.cap_prefix = sa.max_prefix_pages * a.page_size;
     p.cap_rows = a.max_pages * a.page_size;
     p.num_pages = a.num_pages;
-    p.window = a.window;
+    p.window = std::min(a.window, INT32_MAX - 64);           // (positions start at -T: no wrap)
     p.np = w.np;
     p.n_rt = w.n_rt;
     p.logit_scale_log2 = a.softmax_scale / static_cast<float>(D) * kLog2e;
-    p.stat = part.stat;
-    p.o = part.o;
+    p.stat = reinterpret_cast<float2*>(ws + w.pre_stat);
+    p.o = reinterpret_cast<float*>(ws + w.pre_o);
     CUtensorMap tk, tv;
     const bool ok = MX ? encode_cache_mx(&tk, a.k_cache, a.num_pages, a.Hk, a.page_size, D) &&
                              encode_cache_mx(&tv, a.v_cache, a.num_pages, a.Hk, a.page_size, D)
@@ -1065,74 +1700,115 @@ cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, const
                                         : encode_cache(&tv, a.v_cache, a.num_pages, a.Hk, a.page_size, D));
     if (!ok) return cudaErrorInvalidValue;
     auto kern = prefix_kernel<D, MX, RG>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(w.np, w.n_rt * a.Hk), dim3(kThreads), kSmem, s, tk, tv, p);
 }
 
-}  // namespace
-
-size_t decode_shared_ws_bytes(int B, int T, int H, int Hk, int D) { return shared_plan(B, T, H, Hk, D).bytes; }
-
-cudaError_t launch_decode_shared(const DecodeSharedArgs& sa, cudaStream_t s) {
+template <int D, bool MX>
+cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     const DecodeArgs& a = sa.d;
-    const SharedPlan w = shared_plan(a.B, a.T, a.H, a.Hk, a.D);
+    const SharedPlan w = shared_plan(a.B, a.T, a.H, a.Hk, D);
+    const bool few = w.pre_rows == kFewRows;
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
-    SharedPart part = {};
-    part.prefix_table = sa.prefix_table;
-    part.prefix_len = sa.prefix_len;
-    part.max_prefix_pages = sa.max_prefix_pages;
-    part.pre = 1;
-    part.nsplit = w.np;
-    part.n_rt = w.n_rt;
-    part.stat = reinterpret_cast<float2*>(ws + w.pre_stat);
-    part.o = reinterpret_cast<float*>(ws + w.pre_o);
-    cudaError_t e;
-    if (w.pre_rows == kFewRows) {
-        e = launch_decode_part(a, part, s);
-    } else if (w.pre_rows == 128) {
-        e = a.mx ? launch_prefix<128, true, 1>(sa, w, part, s)
-                 : (a.D == 128 ? launch_prefix<128, false, 1>(sa, w, part, s)
-                               : launch_prefix<64, false, 1>(sa, w, part, s));
-    } else {
-        e = a.mx ? launch_prefix<128, true, 2>(sa, w, part, s)
-                 : (a.D == 128 ? launch_prefix<128, false, 2>(sa, w, part, s)
-                               : launch_prefix<64, false, 2>(sa, w, part, s));
+    QueryParams q = {};
+    q.q = static_cast<const uint16_t*>(a.q.ptr);
+    q.qs0 = a.q.stride[0];
+    q.qs1 = a.q.stride[1];
+    q.qs2 = a.q.stride[2];
+    q.qs3 = a.q.stride[3];
+    q.q_vec = view_vec8(a.q) ? 1 : 0;
+    q.G = a.H / a.Hk;
+    q.R = a.T * q.G;
+    q.n_rows = a.B * q.R;
+    q.rows_pad = w.rows_pad;
+    q.codes = ws + w.codes;
+    q.img = few ? nullptr : ws + w.img;
+    q.scale = reinterpret_cast<float*>(ws + w.q_scale);
+    cudaError_t e = launch_pdl(query_kernel<D, MX>, dim3((unsigned)ceil_div(q.n_rows, 32), a.Hk), dim3(128), 0, s, q);
+    if (e != cudaSuccess) return e;
+    if (!few) {
+        e = w.pre_rows == 128 ? launch_prefix<D, MX, 1>(sa, w, s) : launch_prefix<D, MX, 2>(sa, w, s);
+        if (e != cudaSuccess) return e;
     }
+    RowsParams r = {};
+    r.q8 = q.codes;
+    r.q_scale = q.scale;
+    r.kc = a.k_cache;
+    r.vc = a.v_cache;
+    r.ksc = a.k_scale;
+    r.vsc = a.v_scale;
+    r.ksf = a.k_sf;
+    r.vsf = a.v_sf;
+    r.per_tensor = (a.kv_flags & 1) ? 1 : 0;
+    r.sc_vec = reinterpret_cast<uintptr_t>(a.k_scale) % 16 == 0 && reinterpret_cast<uintptr_t>(a.v_scale) % 16 == 0;
+    r.ptab = a.page_table;
+    r.prefix = sa.prefix_table;
+    r.plen = sa.prefix_len;
+    r.ctx = a.ctx_lens;
+    r.B = a.B;
+    r.T = a.T;
+    r.Hk = a.Hk;
+    r.G = q.G;
+    r.R = q.R;
+    r.n_rows = q.n_rows;
+    r.rows_pad = w.rows_pad;
+    r.lg_page = 31 - __builtin_clz(static_cast<unsigned>(a.page_size));
+    r.max_pages = a.max_pages;
+    r.cap_prefix = sa.max_prefix_pages * a.page_size;
+    r.num_pages = a.num_pages;
+    r.window = std::min(a.window, INT32_MAX - 64);
+    r.np = few ? w.np : 0;
+    r.ns = w.ns;
+    r.logit_scale_log2 = a.softmax_scale / static_cast<float>(D) * kLog2e;
+    r.pre_stat = reinterpret_cast<float2*>(ws + w.pre_stat);
+    r.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
+    r.own_stat = reinterpret_cast<float2*>(ws + w.own_stat);
+    r.own_o = reinterpret_cast<float*>(ws + w.own_o);
+    r.late_wait = few ? 0 : 1;
+    const dim3 grid((unsigned)(r.np * a.Hk + (int64_t)w.ns * a.B * a.Hk)), block(32 * kRowsWarps);
+    if (!MX && (a.kv_flags & 2)) e = launch_pdl(rows_kernel<D, false, true>, grid, block, 0, s, r);
+    else e = launch_pdl(rows_kernel<D, MX, false>, grid, block, 0, s, r);
     if (e != cudaSuccess) return e;
     MergeParams m = {};
-    m.pre_stat = part.stat;
-    m.pre_o = part.o;
-    part.pre = 0;
-    part.nsplit = w.ns;
-    part.stat = reinterpret_cast<float2*>(ws + w.own_stat);
-    part.o = reinterpret_cast<float*>(ws + w.own_o);
-    part.late_wait = 1;
-    e = launch_decode_part(a, part, s);
-    if (e != cudaSuccess) return e;
-    m.own_stat = part.stat;
-    m.own_o = part.o;
+    m.pre_stat = r.pre_stat;
+    m.pre_o = r.pre_o;
+    m.own_stat = r.own_stat;
+    m.own_o = r.own_o;
     m.plen = sa.prefix_len;
-    m.cap_prefix = sa.max_prefix_pages * a.page_size;
+    m.cap_prefix = r.cap_prefix;
     m.np = w.np;
     m.ns = w.ns;
     m.pre_rows = w.pre_rows;
     m.n_rt = w.n_rt;
+    m.unit = few ? kBlk : kKeys;
+    m.at_once = few ? kRowsWarps / (int)ceil_div(q.n_rows, 16) : kMinTiles;
     m.T = a.T;
-    m.G = a.H / a.Hk;
-    m.R = a.T * m.G;
-    m.n_rows = a.B * m.R;
+    m.G = q.G;
+    m.R = q.R;
+    m.n_rows = q.n_rows;
     m.Hk = a.Hk;
     m.out = static_cast<__nv_bfloat16*>(a.out);
     m.os0 = a.out_stride[0];
     m.os1 = a.out_stride[1];
     m.os2 = a.out_stride[2];
     m.os3 = a.out_stride[3];
-    const dim3 grid((unsigned)ceil_div(m.n_rows, 32), (unsigned)(a.D / kCh), (unsigned)a.Hk);
     // a plain stream-ordered launch: it starts after both parts
-    if (a.D == 128) shared_merge_kernel<128><<<grid, 256, 0, s>>>(m);
-    else shared_merge_kernel<64><<<grid, 256, 0, s>>>(m);
+    shared_merge_kernel<D><<<dim3((unsigned)ceil_div(m.n_rows, 32), D / kCh, a.Hk), 256, 0, s>>>(m);
     return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t decode_shared_ws_bytes(int B, int T, int H, int Hk, int D) { return shared_plan(B, T, H, Hk, D).bytes; }
+
+cudaError_t launch_decode_shared(const DecodeSharedArgs& a, cudaStream_t s) {
+    if (a.d.mx) return a.d.D == 128 ? launch_shared_d<128, true>(a, s) : cudaErrorInvalidValue;
+    switch (a.d.D) {
+        case 64: return launch_shared_d<64, false>(a, s);
+        case 128: return launch_shared_d<128, false>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 unsigned read_clear_shared_error() {

@@ -411,6 +411,48 @@ def test_shared_graph_follows_the_lengths(handles):
         check_shared(out, d, 9999, 0.09)
 
 
+@pytest.mark.parametrize("B,T,H,Hk,D,page,prefix,ctx,fmt", [
+    (3, 2, 16, 1, 128, 64, 500, [502, 700, 650], "token"), (3, 1, 16, 2, 64, 16, 77, [78, 0, 90], "token"),
+    (9, 4, 16, 1, 128, 32, 500, [504 + 31 * i for i in range(9)], "token"),
+    (5, 4, 16, 1, 64, 128, 300, [304 + 31 * i for i in range(5)], "token_vt"),
+    (9, 2, 16, 1, 128, 128, 300, [302 + 31 * i for i in range(9)], "tensor_vt"),
+    (2, 1, 16, 1, 128, 128, 300, [302, 1], "token_vt"),
+    (9, 2, 16, 1, 128, 16, 300, [302 + 31 * i for i in range(9)], "mxfp4"),
+])
+def test_shared_slots_without_a_key_may_hold_anything(handles, B, T, H, Hk, D, page, prefix, ctx, fmt):
+    """NaN codes and NaN or infinite scales behind a sequence's end, behind the
+    prefix's end, before a sequence's first own token, and in unused pages (page
+    0 among them) change nothing."""
+    d = sh.make_shared(B, T, H, Hk, D, page, prefix, ctx, seed=77, fmt=fmt)
+    # page 0 unused: its tokens move to a page of their own
+    spare = d["pages"]
+    for n in ("kc", "vc") + (() if fmt.startswith("tensor") else ("ks", "vs")):
+        d[n] = torch.cat((d[n], d[n][:1]))
+    d["pages"] += 1
+    d["prefix"] = torch.where(d["prefix"] == 0, spare, d["prefix"]).int()
+    d["table"] = torch.where(d["table"] == 0, spare, d["table"]).int()
+    used = np.zeros((d["pages"], page), bool)
+    for j in range(prefix):
+        used[d["prefix"][j // page], j % page] = True
+    for b in range(B):
+        for j in range(prefix, ctx[b]):
+            used[d["table"][b, j // page], j % page] = True
+    dead = torch.from_numpy(~used)
+    for n in ("k", "v"):
+        c = d[n + "c"]
+        if n == "v" and fmt.endswith("vt"):
+            c = c.transpose(2, 3)
+        c.copy_(torch.where(dead[:, None, :, None], torch.tensor(127 if n == "k" else 255, dtype=torch.uint8), c))
+        if fmt == "mxfp4":
+            d[n + "s"] = torch.where(dead[:, None, :, None], torch.tensor(255, dtype=torch.uint8), d[n + "s"])
+        elif not fmt.startswith("tensor"):
+            d[n + "s"] = torch.where(dead[:, None, :], float("nan") if n == "k" else float("inf"), d[n + "s"])
+    out = run_shared(handles[D], d, page, 9999, 1.0 / math.sqrt(D))
+    torch.cuda.synchronize()
+    assert sage.sage_device_error() == sage.SAGE_OK
+    check_shared(out, d, 9999, 1.0 / math.sqrt(D))
+
+
 def test_shared_reports_bad_pages_and_lengths(handles):
     d = sh.make_shared(3, 1, 16, 1, 128, 64, 500, [600, 700, 650], seed=2)
     bad = dict(d, prefix=d["prefix"].clone())
