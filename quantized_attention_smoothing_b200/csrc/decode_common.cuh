@@ -126,15 +126,16 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // The cache [num_pages, Hk, page, D] e4m3 as a 3-D map {D bytes, page
-// rows, num_pages * Hk}; one box = one page of one kv head, with the swizzle
-// of a D-byte row (128B or 64B).
-inline bool encode_cache(CUtensorMap* map, const void* ptr, int num_pages, int Hk, int page, int D) {
+// rows, num_pages * Hk}; one box = one page of one kv head (or `box_rows` rows
+// of it), with the swizzle of a D-byte row (128B or 64B).
+inline bool encode_cache(CUtensorMap* map, const void* ptr, int num_pages, int Hk, int page, int D,
+                         int box_rows = 0) {
     auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
     if (!enc) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page),
                                 static_cast<cuuint64_t>(num_pages) * Hk};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(page) * D};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(page), 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(box_rows ? box_rows : page), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -144,30 +145,34 @@ inline bool encode_cache(CUtensorMap* map, const void* ptr, int num_pages, int H
 
 // The transposed V cache [num_pages, Hk, D, page = 128] as a 3-D map
 // {128 key bytes, D channel rows, num_pages * Hk}; one box = one page of
-// one kv head as [channel][key], 128B swizzle.
-inline bool encode_cache_vt(CUtensorMap* map, const void* ptr, int num_pages, int Hk, int D) {
+// one kv head as [channel][key], 128B swizzle (or half a page, `box_keys` 64,
+// 64B swizzle).
+inline bool encode_cache_vt(CUtensorMap* map, const void* ptr, int num_pages, int Hk, int D, int box_keys = kKeys) {
     auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
     if (!enc) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kKeys), static_cast<cuuint64_t>(D),
                                 static_cast<cuuint64_t>(num_pages) * Hk};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(kKeys), static_cast<cuuint64_t>(D) * kKeys};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(kKeys), static_cast<cuuint32_t>(D), 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_keys), static_cast<cuuint32_t>(D), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box_keys == kKeys ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The MXFP4 cache codes [num_pages, Hk, page, D / 2] bytes (two E2M1 codes a
 // byte) as a 3-D map {D / 2 bytes, page rows, num_pages * Hk}; one box = one
-// page of one kv head, 64B swizzle (D = 128: 64-byte rows).
-inline bool encode_cache_mx(CUtensorMap* map, const void* ptr, int num_pages, int Hk, int page, int D) {
+// page of one kv head (or `box_rows` rows of it), 64B swizzle (D = 128:
+// 64-byte rows).
+inline bool encode_cache_mx(CUtensorMap* map, const void* ptr, int num_pages, int Hk, int page, int D,
+                            int box_rows = 0) {
     auto enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
     if (!enc || D != 128) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D / 2), static_cast<cuuint64_t>(page),
                                 static_cast<cuuint64_t>(num_pages) * Hk};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D / 2), static_cast<cuuint64_t>(page) * (D / 2)};
-    const cuuint32_t box[3] = {static_cast<cuuint32_t>(D / 2), static_cast<cuuint32_t>(page), 1};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(D / 2), static_cast<cuuint32_t>(box_rows ? box_rows : page), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(ptr), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,

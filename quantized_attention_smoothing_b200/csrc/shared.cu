@@ -41,11 +41,26 @@ constexpr int kFewRows = 64;                 // rows that rows_kernel takes
 
 // The splits, of at most nsplit, that n key tiles (prefix_kernel) or blocks
 // (rows_kernel) are shared out among: none gets fewer than a CTA works on at
-// once, which would only make more partials to combine.
-__host__ __device__ inline int used_splits(int n, int nsplit, int at_once) {
-    const int want = (n + at_once - 1) / at_once;
+// once (2^lg_at_once), which would only make more partials to combine.
+__host__ __device__ inline int used_splits(int n, int nsplit, int lg_at_once) {
+    const int want = (n + (1 << lg_at_once) - 1) >> lg_at_once;
     return want < 1 ? 1 : (want < nsplit ? want : nsplit);
 }
+
+// The share [first, last) of split `split` of n things among nsp (none for
+// split >= nsp).
+__device__ __forceinline__ void share_out(int n, int nsp, int split, int& first, int& last) {
+    const int q = (int)((unsigned)n / (unsigned)nsp), rem = n - q * nsp, s = min(split, nsp);
+    first = s * q + min(s, rem);
+    last = s < nsp ? first + q + (s < rem ? 1 : 0) : first;
+}
+
+// n / d as a multiplication: exact while n d < 2^32 (mul = ceil(2^32 / d)).
+struct FastDiv {
+    uint32_t mul;                            // 0: d = 1
+};
+inline FastDiv fast_div_by(int64_t d) { return {d <= 1 ? 0u : (uint32_t)(((int64_t(1) << 32) + d - 1) / d)}; }
+__device__ __forceinline__ int fast_div(int n, FastDiv d) { return d.mul == 0 ? n : (int)__umulhi((uint32_t)n, d.mul); }
 
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -108,7 +123,7 @@ struct MergeParams {
     const float* own_o;                      // [B Hk][ns][D][64]
     const int32_t* plen;
     int cap_prefix, np, ns, pre_rows, n_rt;
-    int unit, at_once;                       // keys of a tile or block of the prefix part, used_splits' third
+    int unit, lg_at_once;                    // keys of a tile or block of the prefix part, used_splits' third
     int n_rows, R, T, G, Hk;
     __nv_bfloat16* out;
     int64_t os0, os1, os2, os3;
@@ -130,7 +145,7 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) 
     const int nn = in ? n : p.n_rows - 1;
     const int b = nn / p.R, rr = nn % p.R;
     const int L = max(0, min(*p.plen, p.cap_prefix));
-    const int np = L > 0 ? used_splits((L + p.unit - 1) / p.unit, p.np, p.at_once) : 0;
+    const int np = L > 0 ? used_splits((L + p.unit - 1) / p.unit, p.np, p.lg_at_once) : 0;
     const size_t part_p = ((size_t)hk * p.n_rt + nn / p.pre_rows) * p.np, part_o = ((size_t)b * p.Hk + hk) * p.ns;
     const int r = nn % p.pre_rows;
     float M = -INFINITY, l = 0.0f, acc[kCh];
@@ -329,7 +344,7 @@ __global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
 // waiting for both products: 1800 of 5500 cycles a unit spent waiting, and 128
 // logits a thread spilled; 120 us against 62 us for 4096 rows x 32768 keys.)
 constexpr int kScStages = 8;                 // scale ring
-constexpr int kMinTiles = 2;                 // key tiles a CTA has in flight
+constexpr int kLgMinTiles = 1;               // two key tiles: what a CTA has in flight
 constexpr int kThreads = 512;
 constexpr int kConvWarp0 = 8, kTmaWarp = 12, kMmaWarp0 = 13, kScaleWarp = 14, kMmaWarp1 = 15;
 // 256 x 168 + 128 x 96 + 128 x 80 <= 512 x 128 registers, the launch's own
@@ -527,9 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // key tiles [t0, t0 + n_all) that some row of the CTA sees; this split's share
     const int t0 = hi >= 0 ? lo / kKeys : 0;
     const int n_all = hi >= 0 ? hi / kKeys + 1 - t0 : 0;
-    const int nsp = used_splits(n_all, p.np, kMinTiles);
-    const int tb = t0 + (int)((int64_t)min(split, nsp) * n_all / nsp);
-    const int nt = t0 + (int)((int64_t)min(split + 1, nsp) * n_all / nsp) - tb;
+    int tb, te;
+    share_out(n_all, used_splits(n_all, p.np, kLgMinTiles), split, tb, te);
+    const int nt = te - tb;
+    tb += t0;
     const int ppt = kKeys / p.page;
     const size_t part = (size_t)blockIdx.y * p.np + split;
 
@@ -584,8 +600,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // could be NaN codes, which a weight of zero does not cancel
                     const int z = MX || found ? phys * p.Hk + hk : -1, q = lane - slot0;
                     constexpr int kRowB = Sm::kKStage / kKeys;
-                    tma_load_3d(sm + Sm::kK + s * Sm::kKStage + q * p.page * kRowB, &tmK, &bars[Sm::kKvFull + s], 0, 0, z);
-                    tma_load_3d(sm + Sm::kV + s * Sm::kKStage + q * p.page * kRowB, &tmV, &bars[Sm::kKvFull + s], 0, 0, z);
+                    for (int y = 0; y < p.page; y += 64) {                   // boxes of at most 64 rows
+                        const int at = s * Sm::kKStage + (q * p.page + y) * kRowB;
+                        tma_load_3d(sm + Sm::kK + at, &tmK, &bars[Sm::kKvFull + s], 0, y, z);
+                        if (!p.v_trans) tma_load_3d(sm + Sm::kV + at, &tmV, &bars[Sm::kKvFull + s], 0, y, z);
+                    }
+                    if (p.v_trans) tma_load_3d(sm + Sm::kV + s * Sm::kKStage, &tmV, &bars[Sm::kKvFull + s], 0, 0, z);
                     if constexpr (MX) {
                         constexpr int kSfB = D / 32;
                         const int64_t off = (int64_t)z * p.page * kSfB;
@@ -1110,47 +1130,76 @@ __global__ void __launch_bounds__(kThreads, 1)
 // own keys [L, ctx), and, where the whole batch has no more rows than that,
 // all rows against the prefix. With 16 rows a key costs 4 D FLOPs a byte of
 // cache, far from what a tensor pipe is bound by; what counts is latency and
-// bytes in flight. So no TMEM, no shared-memory operands and no roles: a warp
-// takes 16 rows and 64 keys at a time straight from global memory into
-// mma fragments (FP8: QK on the e4m3 codes, PV on fp16; MXFP4: both on bf16),
-// and three CTAs of four independent warps share an SM. (decode.cu's kernel, one CTA an SM, took 27 us for 256 sequences of at
-// most 512 own keys where this takes 8.)
+// bytes in flight. So no TMEM and no roles: a warp takes 16 rows and 64 keys
+// at a time through mma fragments (FP8: QK on the e4m3 codes, PV on fp16;
+// MXFP4: both on bf16), and three CTAs of four independent warps share an SM.
+// One lane copies a warp's blocks (a TMA box of K or V per page, scales by
+// cp.async): the next block's K is on its way while this one's softmax and PV
+// run, the next V while the next QK runs, one stage of each being enough.
+// Pages without a key are read as zeros (a coordinate off the map), and the
+// slots of V without a key are zeroed: a NaN code there must not meet a weight
+// of zero. A call is latency, not throughput: one block a warp and straight
+// code, so what counts is how few instructions there are, at 4 to 7 cycles
+// each. (With the fragments loaded straight from global memory, or with 16-byte
+// cp.async, 64-bit divisions and a rolled epilogue, a call took 19000 cycles
+// for one block a warp; decode.cu's kernel, one CTA an SM, 27 us for 256
+// sequences of at most 512 own keys.)
 // Fragments. The order of the summed index is free as long as both operands
 // have the same, and so is the order of output columns; with thread (g, c) =
 // (lane / 4, lane % 4):
 //   S = Q K^T  summed index: thread c holds the run d = c D / 4 .. of its key
 //              (16 or 32 contiguous bytes), 4 elements a step; column n of
-//              n-tile j is key 16 (n / 2) + 2 j + n % 2 of the block, so that
-//              thread c's columns are the 16 consecutive keys 16 c ..
+//              n-tile j is key 8 j + n, or, over a transposed V, key
+//              16 (n / 2) + 2 j + n % 2, so that thread c's columns are the 16
+//              consecutive keys 16 c ..
 //   O = P V    step s of 16 keys = n-tiles 2 s and 2 s + 1, whose S registers
-//              are P's A operand; thread (g, c) holds V of keys 16 c + 4 s ..
-//              + 3 (V^T: four bytes of a 16-byte run) and channels D g / 8 ..,
-//              one per n-tile, converted exactly in registers.
+//              are P's A operand; thread (g, c) holds V of the keys of its S
+//              columns (V^T: four bytes of a 16-byte run) and channels
+//              D g / 8 .., one per n-tile, converted exactly in registers.
+// With the boxes' swizzles these reads take every bank once, those of a
+// 64-byte V row (V^T) twice.
 constexpr int kBlk = 64;                     // keys a warp takes at a time
 constexpr int kRowsWarps = 4;
 
 struct RowsParams {
     const uint8_t* q8;                       // [Hk][rows_pad][D] e4m3 codes
     const float* q_scale;                    // [Hk][rows_pad]
-    const uint8_t* kc;
-    const uint8_t* vc;
     const float* ksc;
     const float* vsc;
     const uint8_t* ksf;
     const uint8_t* vsf;
-    int per_tensor, sc_vec;                  // scales' base 16-byte aligned
+    int per_tensor;
     const int32_t* ptab;                     // [B, max_pages]
     const int32_t* prefix;
     const int32_t* plen;
     const int32_t* ctx;
     int B, T, Hk, G, R, n_rows, rows_pad, lg_page, max_pages, cap_prefix, num_pages, window;
     int np, ns;                              // splits of the prefix part (0: not here), of a sequence's own
+    FastDiv div_np, div_ns, div_hk, div_r, div_g;
     float logit_scale_log2;
     float2* pre_stat;                        // [Hk][np][64]
     float* pre_o;                            // [Hk][np][D][64]
     float2* own_stat;                        // [B Hk][ns][64]
     float* own_o;
     int late_wait;                           // launched behind prefix_kernel, of which it reads nothing
+};
+
+template <int D, bool MX, bool VT>
+struct SmR {
+    static constexpr int kSteps = MX ? D / 16 : D / 32;              // QK steps
+    static constexpr int kRow = MX ? D / 2 : D;                      // bytes of a cache row
+    static constexpr int kPitch = 17;                                // rows of a staged O
+    static constexpr int kKBytes = kBlk * kRow, kVBytes = VT ? D * kBlk : kBlk * kRow;
+    // a warp's K and V, later its O; then all warps' scales [k | v][64]
+    static constexpr int kStage = al1024(kKBytes + kVBytes > D * kPitch * 4 ? kKBytes + kVBytes : D * kPitch * 4);
+    static constexpr int kScale = kRowsWarps * kStage;
+    static constexpr int kQf = kScale + kRowsWarps * 2 * 4 * kBlk;   // MX: [m-tile][step][lane] query fragments
+    static constexpr int kStat = kQf + (MX ? 4 * kSteps * 32 * 16 : 0);
+    static constexpr int kSpan = kStat + kRowsWarps * 16 * 8;        // lowest, highest key any row sees
+    static constexpr int kBar = kSpan + 8;                           // [warp][k | v], then [warp] abort flags
+    static constexpr int kBytes = kBar + kRowsWarps * 16 + kRowsWarps * 4;
+    static_assert(kKBytes % 1024 == 0 && kBar % 8 == 0, "alignment");
+    static_assert(3 * (kBytes + 2048) <= 228 * 1024, "three CTAs an SM");
 };
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -1174,74 +1223,188 @@ __device__ __forceinline__ void mma_16832_e4m3(float (&c)[4], const uint4& a, ui
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
+// A copy of 4 bytes, the destination zeroed instead where !in.
+__device__ __forceinline__ void cp_async_4_or_zero(void* dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 template <int D, bool MX, bool VT>
-__global__ void __launch_bounds__(32 * kRowsWarps, 3) rows_kernel(const RowsParams p) {
-    constexpr int kSteps = MX ? D / 16 : D / 32; // QK steps
+__global__ void __launch_bounds__(32 * kRowsWarps, 3)
+    rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const RowsParams p) {
+    using Sm = SmR<D, MX, VT>;
+    constexpr int kSteps = Sm::kSteps, kRow = Sm::kRow, kPitch = Sm::kPitch;
     constexpr int kNt = D / 8;                   // n-tiles of O = channels a thread has of a V row
-    constexpr int kKB = MX ? D / 8 : D / 4;      // bytes of a key's row a thread holds
-    constexpr int kRowB = MX ? D / 2 : D;
-    constexpr int kVB = MX ? D / 16 : D / 8;     // bytes of a value's row
-    constexpr int kPitch = 17;                   // rows of a staged O
-    __shared__ __align__(16) float o_s[kRowsWarps][D * kPitch];
-    __shared__ float2 stat_s[kRowsWarps][16];
-    __shared__ int lo_s, hi_s;
-    uint4* qf = reinterpret_cast<uint4*>(&o_s[0][0]);         // [m-tile][step][lane] (until O is staged)
-    static_assert(!MX || 4 * kSteps * 32 * 16 <= sizeof(o_s), "query fragments");
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    uint8_t* st = sm + warp * Sm::kStage;
+    float* sc = reinterpret_cast<float*>(sm + Sm::kScale) + warp * 2 * kBlk;
+    uint4* qf = reinterpret_cast<uint4*>(sm + Sm::kQf);
+    auto stat_s = reinterpret_cast<float2(*)[16]>(sm + Sm::kStat);
+    int* span = reinterpret_cast<int*>(sm + Sm::kSpan);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Sm::kBar) + 2 * warp;
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + Sm::kBar + kRowsWarps * 16) + warp;
+    if (lane == 0) {
+        mbar_init(&bar[0], 1);
+        mbar_init(&bar[1], 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
     if (!p.late_wait) pdl_wait();
     pdl_launch_dependents();
 
     const bool pre = (int)blockIdx.x < p.np * p.Hk;
     const int bi = pre ? blockIdx.x : blockIdx.x - p.np * p.Hk;
     const int nsplit = pre ? p.np : p.ns;
-    const int item = bi / nsplit, split = bi % nsplit;
-    const int hk = pre ? item : item % p.Hk, b = pre ? 0 : item / p.Hk;
+    const int item = fast_div(bi, pre ? p.div_np : p.div_ns), split = bi - item * nsplit;
+    const int b = pre ? 0 : fast_div(item, p.div_hk), hk = item - b * p.Hk;
     const int rows = pre ? p.n_rows : p.R;
     const int n0 = b * p.R;                                   // first row (pre: b = 0)
+    // warps: m-tile (16 rows) x key slice
+    const int mts = (rows + 15) >> 4, lg_slices = mts == 1 ? 2 : (mts == 2 ? 1 : 0), slices = 1 << lg_slices;
+    const int mt = warp >> lg_slices, slice = warp & (slices - 1);
+    const bool live = mt < mts;
+    // everything the set-up reads, requested together
     int L = *p.plen;
+    const int r0 = 16 * mt + g;
+    int ctx[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+        ctx[r] = pre ? (r0 + 8 * r < rows ? __ldg(p.ctx + fast_div(r0 + 8 * r, p.div_r)) : 0) : __ldg(p.ctx + b);
+    uint4 u[2][D / 64];
+    float cq[2];                                 // base-2 logit = (S k_scale) cq; > 0 keeps a masked -inf
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        const bool in = live && r0 + 8 * r < rows;
+        const size_t n = (size_t)hk * p.rows_pad + n0 + r0 + 8 * r;
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k)
+            u[r][k] = in ? __ldcg(reinterpret_cast<const uint4*>(p.q8 + n * D + c * (D / 4)) + k)
+                         : make_uint4(0u, 0u, 0u, 0u);
+        cq[r] = in ? __ldcg(p.q_scale + n) : 0.0f;
+    }
+    const float ks_t = !MX && p.per_tensor ? __ldg(p.ksc) : 1.0f, vs_t = !MX && p.per_tensor ? __ldg(p.vsc) : 1.0f;
+
     if (L < 0 || L > p.cap_prefix) {
         if (tid == 0 && split == 0) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
         L = max(0, min(L, p.cap_prefix));
     }
     const int cap = p.max_pages << p.lg_page;
-    // keys that row r sees of this part
-    auto see = [&](int r, int& klo, int& khi) {
-        klo = INT32_MAX;
-        khi = -1;
-        if (r < rows) {
-            const int n = n0 + r;
-            const int ctx = max(0, min(__ldg(p.ctx + n / p.R), cap));
-            const int pq = ctx - p.T + (n % p.R) / p.G;
+    if (!pre && tid == 0 && split == 0 && (ctx[0] < 0 || ctx[0] > cap)) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
+    // keys that rows r0 and r0 + 8 see of this part
+    int klo[2], khi[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        klo[r] = INT32_MAX;
+        khi[r] = -1;
+        if (r0 + 8 * r < rows) {
+            ctx[r] = max(0, min(ctx[r], cap));
+            const int n = r0 + 8 * r, rr = pre ? n - fast_div(n, p.div_r) * p.R : n;
+            const int pq = ctx[r] - p.T + fast_div(rr, p.div_g);
             const int a = max(pre ? 0 : L, pq - p.window + 1), e = pre ? min(pq, L - 1) : pq;
             if (e >= a) {
-                klo = a;
-                khi = e;
+                klo[r] = a;
+                khi[r] = e;
             }
         }
-    };
-    if (!pre && tid == 0 && split == 0) {
-        const int ctx = __ldg(p.ctx + b);
-        if (ctx < 0 || ctx > cap) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
     }
-    // warps: m-tile (16 rows) x key slice
-    const int mts = (rows + 15) >> 4, slices = kRowsWarps / mts;
-    const int mt = warp / slices, slice = warp % slices;
-    const bool live = mt < mts;
-    int klo[2], khi[2];
-    see(16 * mt + g, klo[0], khi[0]);
-    see(16 * mt + g + 8, klo[1], khi[1]);
-    if (tid == 0) {
-        lo_s = INT32_MAX;
-        hi_s = -1;
-    }
-    __syncthreads();
-    {
-        const int lo = __reduce_min_sync(0xffffffffu, live ? min(klo[0], klo[1]) : INT32_MAX);
-        const int hi = __reduce_max_sync(0xffffffffu, live ? max(khi[0], khi[1]) : -1);
-        if (lane == 0) {
-            atomicMin(&lo_s, lo);
-            atomicMax(&hi_s, hi);
+    // [lo, hi]: keys that any row sees (a sequence's T rows see all of its keys
+    // from the first one's window on)
+    int lo, hi;
+    if (pre) {
+        if (tid == 0) {
+            span[0] = INT32_MAX;
+            span[1] = -1;
         }
+        __syncthreads();
+        lo = __reduce_min_sync(0xffffffffu, live ? min(klo[0], klo[1]) : INT32_MAX);
+        hi = __reduce_max_sync(0xffffffffu, live ? max(khi[0], khi[1]) : -1);
+        if (lane == 0) {
+            atomicMin(span, lo);
+            atomicMax(span + 1, hi);
+        }
+        __syncthreads();
+        lo = span[0];
+        hi = span[1];
+    } else {
+        const int x = max(0, min(ctx[0], cap));
+        lo = max(max(L, 0), x - p.T - p.window + 1);
+        hi = lo < x ? x - 1 : -1;
+    }
+    const int blk0 = hi >= 0 ? lo / kBlk : 0, n_all = hi >= 0 ? hi / kBlk + 1 - blk0 : 0;
+    int first, last;
+    share_out(n_all, used_splits(n_all, nsplit, lg_slices), split, first, last);
+    first += blk0;
+    last += blk0;
+
+    const int32_t* tab = pre ? p.prefix : p.ptab + (int64_t)b * p.max_pages;
+    const int lgp = min(p.lg_page, 6);                        // keys of one page inside a block (log2)
+    // Pages of a block, lane i holding page i: its number, or -1 where it holds
+    // no key of [lo, hi] or is off the cache (bad)
+    struct Pages {
+        int k0, phys;
+        bool bad;
+    };
+    auto lookup = [&](int blk) {
+        Pages f{blk * kBlk, -1, false};
+        const int lp = (f.k0 >> p.lg_page) + lane;
+        if (lane < (kBlk >> lgp) && (lp << p.lg_page) <= hi && ((lp + 1) << p.lg_page) > lo) {
+            f.phys = __ldg(tab + lp);
+            f.bad = f.phys < 0 || f.phys >= p.num_pages;
+        }
+        return f;
+    };
+    // a block's K (V) codes and scales into the stage
+    auto copy = [&](const Pages& f, bool v) {
+        const bool found = f.phys >= 0 && !f.bad;
+        const int in0 = f.k0 & ((1 << p.lg_page) - 1);        // block's offset in a larger page
+        if (lane == 0) mbar_arrive_expect_tx(&bar[v], v ? Sm::kVBytes : Sm::kKBytes);
+        __syncwarp();
+        if (lane < (kBlk >> lgp)) {
+            const int z = found ? f.phys * p.Hk + hk : -1;
+            uint8_t* dst = st + (v ? Sm::kKBytes : 0) + (lane << lgp) * kRow;
+            if (VT && v) tma_load_3d(dst, &tmV, &bar[1], in0, 0, z);
+            else tma_load_3d(dst, v ? &tmV : &tmK, &bar[v], 0, in0, z);
+        }
+        if (MX || !p.per_tensor) {
+            const uint8_t* src = MX ? (v ? p.vsf : p.ksf) : reinterpret_cast<const uint8_t*>(v ? p.vsc : p.ksc);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int o = lane + 32 * i;
+                const int pg = __shfl_sync(0xffffffffu, found ? f.phys : -1, o >> lgp);
+                const int64_t t = (((int64_t)max(pg, 0) * p.Hk + hk) << p.lg_page) + in0 + (o & ((1 << lgp) - 1));
+                cp_async_4_or_zero(sc + (v ? kBlk : 0) + o, src + 4 * t, pg >= 0 && f.k0 + o >= lo && f.k0 + o <= hi);
+            }
+        }
+        cp_async_commit();
+    };
+    uint32_t phase[2] = {0, 0};
+    bool ok = true;
+    int landing = 0;                                          // copies in flight: 1 K, 2 V
+    // K (V) of the present block has landed
+    auto landed = [&](int v) {
+        ok = warp_all(mbar_wait(&bar[v], phase[v], abort_flag, &g_shared_err, 15));
+        if (!ok) return;
+        phase[v] ^= 1;
+        landing &= ~(1 << v);
+        cp_async_wait<1>();
+        __syncwarp();
+    };
+    Pages pg = {0, -1, false};
+    __syncwarp();
+    if (live && first + slice < last) {
+        pg = lookup(first + slice);
+        copy(pg, false);
+        copy(pg, true);
+        landing = 3;
     }
     // the query codes as A fragments, thread (g, c) holding the run c D / 4 ..
     // of rows g and g + 8: e4m3 as they are; for an MXFP4 cache their exact
@@ -1249,53 +1412,31 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) rows_kernel(const RowsPara
     // orders K's, in shared memory
     uint4 qa[MX ? 1 : kSteps];
     {
-        const uint8_t* src = p.q8 + ((size_t)hk * p.rows_pad + n0 + 16 * mt + g) * D + c * (D / 4);
-        uint4 u[2][D / 64];
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int k = 0; k < D / 64; ++k)
-                u[r][k] = live && 16 * mt + g + 8 * r < rows
-                              ? __ldcg(reinterpret_cast<const uint4*>(src + 8 * r * D) + k)
-                              : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t* w0 = reinterpret_cast<const uint32_t*>(u[0]);
         const uint32_t* w1 = reinterpret_cast<const uint32_t*>(u[1]);
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
+        for (int s = 0; s < kSteps; ++s) {
             if constexpr (MX) {
-                const int k = st & ~1;
+                const int k = s & ~1;
                 uint4 a;
-                if ((st & 1) == 0)
+                if ((s & 1) == 0)
                     a = make_uint4(e4m3_pick_to_bf16x2<0>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<0>(w1[k], w1[k + 1]),
                                    e4m3_pick_to_bf16x2<1>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<1>(w1[k], w1[k + 1]));
                 else
                     a = make_uint4(e4m3_pick_to_bf16x2<2>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<2>(w1[k], w1[k + 1]),
                                    e4m3_pick_to_bf16x2<3>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<3>(w1[k], w1[k + 1]));
-                if (live && slice == 0) qf[(mt * kSteps + st) * 32 + lane] = a;
+                if (live && slice == 0) qf[(mt * kSteps + s) * 32 + lane] = a;
             } else {
-                qa[st] = make_uint4(w0[2 * st], w1[2 * st], w0[2 * st + 1], w1[2 * st + 1]);
+                qa[s] = make_uint4(w0[2 * s], w1[2 * s], w0[2 * s + 1], w1[2 * s + 1]);
             }
         }
     }
-    float cq[2] = {FLT_MIN, FLT_MIN};            // base-2 logit = (S k_scale) cq; > 0 keeps a masked -inf
-    if (live) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-            if (16 * mt + g + 8 * r < rows)
-                cq[r] = fmaxf(__ldcg(p.q_scale + (size_t)hk * p.rows_pad + n0 + 16 * mt + g + 8 * r) * p.logit_scale_log2,
-                              FLT_MIN);
-    }
-    const float ks_t = !MX && p.per_tensor ? __ldg(p.ksc) : 1.0f, vs_t = !MX && p.per_tensor ? __ldg(p.vsc) : 1.0f;
-    __syncthreads();
-    const int lo = lo_s, hi = hi_s;
-    const int blk0 = hi >= 0 ? lo / kBlk : 0, n_all = hi >= 0 ? hi / kBlk + 1 - blk0 : 0;
-    const int nsp = used_splits(n_all, nsplit, slices);
-    const int first = blk0 + (int)((int64_t)min(split, nsp) * n_all / nsp);
-    const int last = blk0 + (int)((int64_t)min(split + 1, nsp) * n_all / nsp);
+    for (int r = 0; r < 2; ++r) cq[r] = fmaxf(cq[r] * p.logit_scale_log2, FLT_MIN);
+    if (MX) __syncthreads();
 
-    const int32_t* tab = pre ? p.prefix : p.ptab + (int64_t)b * p.max_pages;
-    const int end_tok = pre ? L : hi + 1;                     // pages from here on hold no key of the part
-    const int lgp = min(p.lg_page, 6);                        // keys of one page inside a block (log2)
+    // key (of the block) of element x of this thread's pair in n-tile j
+    auto key_of = [&](int j, int x) { return VT ? 16 * c + 2 * j + x : 8 * j + 2 * c + x; };
     float O[kNt][4];
 #pragma unroll
     for (int t = 0; t < kNt; ++t)
@@ -1305,140 +1446,72 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) rows_kernel(const RowsPara
     int vexp = kNoExp;                                        // FP8: O is in units of 2^vexp
     for (int blk = first + slice; live && blk < last; blk += slices) {
         const int k0 = blk * kBlk;
-        // pages of the block: lane i holds page i
-        int phys = 0;
-        bool bad = false;
-        {
-            const int lp = (k0 >> p.lg_page) + lane;
-            if (lane < (kBlk >> lgp) && (lp << p.lg_page) < end_tok && ((lp + 1) << p.lg_page) > lo) {
-                const int pg = __ldg(tab + lp);
-                bad = pg < 0 || pg >= p.num_pages;
-                if (bad) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
-                else phys = pg;
-            }
-        }
-        const unsigned badm = __ballot_sync(0xffffffffu, bad);
-        const int in0 = k0 & ((1 << p.lg_page) - 1);          // block's offset in a larger page
-        // (page, head, offset) index of key o of the block
-        auto token = [&](int o) -> int64_t {
-            const int pg = __shfl_sync(0xffffffffu, phys, o >> lgp);
-            return (((int64_t)pg * p.Hk + hk) << p.lg_page) + in0 + (o & ((1 << lgp) - 1));
-        };
+        const bool more = blk + slices < last;
+        Pages next = {0, -1, false};
+        if (more) next = lookup(blk + slices);
+        const unsigned badm = __ballot_sync(0xffffffffu, pg.bad);
+        if (pg.bad) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
         // ---- S = Q K^T
+        landed(0);
+        if (!ok) break;
         float S[8][4];
 #pragma unroll
-        for (int jh = 0; jh < 2; ++jh) {
-            uint4 kr[4][MX ? 1 : D / 64];
-            uint32_t ke[4];
+        for (int j = 0; j < 8; ++j) {
+            const int o = VT ? 16 * (g >> 1) + 2 * j + (g & 1) : 8 * j + g;
+            uint4 kr[MX ? 1 : D / 64];
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-                const int64_t tk = token(16 * (g >> 1) + 2 * (4 * jh + jj) + (g & 1));
-                const uint4* src = reinterpret_cast<const uint4*>(p.kc + tk * kRowB + c * kKB);
+            for (int k = 0; k < (MX ? 1 : D / 64); ++k)
+                kr[k] = *reinterpret_cast<const uint4*>(st + o * kRow + (e4m3_chunk<kRow>((MX ? 1 : D / 64) * c + k, o) << 4));
 #pragma unroll
-                for (int k = 0; k < (MX ? 1 : D / 64); ++k) kr[jj][k] = __ldg(src + k);
-                ke[jj] = MX ? __ldg(p.ksf + tk * 4 + c) : 0u;
-            }
-#pragma unroll
-            for (int jj = 0; jj < 4; ++jj)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) S[4 * jh + jj][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) S[j][e] = 0.0f;
             if constexpr (MX) {
-                uint32_t kb[4][16];
+                uint32_t kb[16];
+                e2m1_block_to_bf16(kr[0], reinterpret_cast<const uint8_t*>(sc)[4 * o + c], kb);
 #pragma unroll
-                for (int jj = 0; jj < 4; ++jj) e2m1_block_to_bf16(kr[jj][0], ke[jj], kb[jj]);
-#pragma unroll
-                for (int st = 0; st < kSteps; ++st) {
-                    const uint4 a = qf[(mt * kSteps + st) * 32 + lane];
-#pragma unroll
-                    for (int jj = 0; jj < 4; ++jj) mma_16816(S[4 * jh + jj], a, kb[jj][2 * st], kb[jj][2 * st + 1]);
-                }
+                for (int s = 0; s < kSteps; ++s)
+                    mma_16816(S[j], qf[(mt * kSteps + s) * 32 + lane], kb[2 * s], kb[2 * s + 1]);
             } else {
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(kr);
 #pragma unroll
-                for (int st = 0; st < kSteps; ++st)
-#pragma unroll
-                    for (int jj = 0; jj < 4; ++jj) {
-                        const uint32_t* w = reinterpret_cast<const uint32_t*>(kr[jj]);
-                        mma_16832_e4m3(S[4 * jh + jj], qa[st], w[2 * st], w[2 * st + 1]);
-                    }
+                for (int s = 0; s < kSteps; ++s) mma_16832_e4m3(S[j], qa[s], w[2 * s], w[2 * s + 1]);
             }
         }
         // ---- scales of keys 16 c .., masks, maxima
-        float vs[16];
         if constexpr (!MX) {
-            const int64_t tk = token(16 * c);                 // (16 consecutive keys are in one page)
             if (p.per_tensor) {
-#pragma unroll
-                for (int k = 0; k < 16; ++k) vs[k] = vs_t;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) S[j][e] *= ks_t;
-            } else if (p.sc_vec) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float4 s = __ldg(reinterpret_cast<const float4*>(p.ksc + tk) + k);
-                    const float4 v = __ldg(reinterpret_cast<const float4*>(p.vsc + tk) + k);
-                    S[2 * k][0] *= s.x;
-                    S[2 * k][1] *= s.y;
-                    S[2 * k][2] *= s.x;
-                    S[2 * k][3] *= s.y;
-                    S[2 * k + 1][0] *= s.z;
-                    S[2 * k + 1][1] *= s.w;
-                    S[2 * k + 1][2] *= s.z;
-                    S[2 * k + 1][3] *= s.w;
-                    vs[4 * k] = v.x;
-                    vs[4 * k + 1] = v.y;
-                    vs[4 * k + 2] = v.z;
-                    vs[4 * k + 3] = v.w;
-                }
             } else {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float s = __ldg(p.ksc + tk + k);
-                    vs[k] = __ldg(p.vsc + tk + k);
-                    S[k >> 1][k & 1] *= s;
-                    S[k >> 1][2 + (k & 1)] *= s;
+                for (int j = 0; j < 8; ++j) {
+                    const float2 s = *reinterpret_cast<const float2*>(sc + key_of(j, 0));
+                    S[j][0] *= s.x;
+                    S[j][1] *= s.y;
+                    S[j][2] *= s.x;
+                    S[j][3] *= s.y;
                 }
             }
         }
-        const bool bad_c = (badm >> ((16 * c) >> lgp)) & 1;
-        // of keys 16 c .. this thread's, no row sees those outside [va, ve]
-        const int va = lo - k0 - 16 * c, ve = bad_c ? -1 : hi - k0 - 16 * c;
-        const bool edge = !__all_sync(0xffffffffu, va <= 0 && ve >= 15);
-        if constexpr (!MX) {
-            // value scales relative to 2^vexp, zero where no row sees the key
-            if (edge) {
-#pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (k < va || k > ve) vs[k] = 0.0f;
-            }
-            float vmax = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) vmax = fmax3(vmax, vs[k], vs[k + 1]);
-            vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
-            vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-            const int ne = scale_exp(vexp, vmax);
-            if (ne != vexp) {
-                if (vexp != kNoExp) {
-                    const float f = pow2i(vexp - ne);
-#pragma unroll
-                    for (int t = 0; t < kNt; ++t)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) O[t][x] *= f;
-                }
-                vexp = ne;
-            }
-            const float f = vexp == kNoExp ? 0.0f : pow2i(-vexp);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) vs[k] *= f;
+        __syncwarp();
+        if (more) {
+            copy(next, false);                                // K's stage is free
+            landing |= 1;
+        } else {
+            cp_async_commit();
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int a = klo[r] - k0 - 16 * c, e = khi[r] - k0 - 16 * c;    // key 16 c + k is seen for a <= k <= e
-            if (!__all_sync(0xffffffffu, a <= 0 && e >= 15 && !bad_c)) {
+            const int a = klo[r] - k0, e = khi[r] - k0;       // key o of the block is seen for a <= o <= e
+            if (!__all_sync(0xffffffffu, a <= 0 && e >= kBlk - 1 && badm == 0)) {
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if (k < a || k > e || bad_c) S[k >> 1][2 * r + (k & 1)] = -INFINITY;
+                for (int j = 0; j < 8; ++j)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int o = key_of(j, x);
+                        if (o < a || o > e || ((badm >> (o >> lgp)) & 1)) S[j][2 * r + x] = -INFINITY;
+                    }
             }
             float mx = -INFINITY;
 #pragma unroll
@@ -1462,7 +1535,54 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) rows_kernel(const RowsPara
             for (int k = 0; k < 16; ++k) {
                 const float x = ex2_approx(fmaf(S[k >> 1][2 * r + (k & 1)], cq[r], -sub));
                 l[r] += x;
-                S[k >> 1][2 * r + (k & 1)] = MX ? x : x * vs[k];
+                S[k >> 1][2 * r + (k & 1)] = x;
+            }
+        }
+        landed(1);
+        if (!ok) break;
+        // slots of found pages that no row sees: zeros (of a transposed V, below)
+        const bool edge = lo > k0 || hi < k0 + kBlk - 1;
+        if (!MX && !VT && edge) {
+            for (int o = lane; o < kBlk; o += 32)
+                if (k0 + o < lo || k0 + o > hi) {
+#pragma unroll
+                    for (int i = 0; i < kRow / 16; ++i)
+                        *reinterpret_cast<uint4*>(st + Sm::kKBytes + o * kRow + 16 * i) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            fence_proxy_async_smem();                         // (before the next copy into the stage)
+            __syncwarp();
+        }
+        if constexpr (!MX) {
+            // value scales relative to 2^vexp (those of slots without a key are zero)
+            float vs[16];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 x = p.per_tensor ? make_float2(vs_t, vs_t)
+                                              : *reinterpret_cast<const float2*>(sc + kBlk + key_of(j, 0));
+                vs[2 * j] = x.x;
+                vs[2 * j + 1] = x.y;
+            }
+            float vmax = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) vmax = fmax3(vmax, vs[k], vs[k + 1]);
+            vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
+            vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+            const int ne = scale_exp(vexp, vmax);
+            if (ne != vexp) {
+                if (vexp != kNoExp) {
+                    const float f = pow2i(vexp - ne);
+#pragma unroll
+                    for (int t = 0; t < kNt; ++t)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) O[t][x] *= f;
+                }
+                vexp = ne;
+            }
+            const float f = vexp == kNoExp ? 0.0f : pow2i(-vexp);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                S[k >> 1][k & 1] *= vs[k] * f;
+                S[k >> 1][2 + (k & 1)] *= vs[k] * f;
             }
         }
         // ---- O += P V
@@ -1472,76 +1592,56 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) rows_kernel(const RowsPara
             for (int s = 0; s < 4; ++s)
                 pa[s] = make_uint4(f16x2(S[2 * s][0], S[2 * s][1]), f16x2(S[2 * s][2], S[2 * s][3]),
                                    f16x2(S[2 * s + 1][0], S[2 * s + 1][1]), f16x2(S[2 * s + 1][2], S[2 * s + 1][3]));
-            const int pg = __shfl_sync(0xffffffffu, phys, 0);
-            const uint8_t* src = p.vc + (((int64_t)pg * p.Hk + hk) * D + kNt * g) * 128 + in0 + 16 * c;
+            // of keys 16 c .., no row sees those outside [va, ve]
+            const int va = lo - k0 - 16 * c, ve = hi - k0 - 16 * c;
 #pragma unroll
-            for (int t0 = 0; t0 < kNt; t0 += 4) {
-                uint4 u[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) u[t] = __ldg(reinterpret_cast<const uint4*>(src + (t0 + t) * 128));
-                if (edge) {                                   // (a NaN code times a weight of 0 is not 0)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        u[t].x &= low_bytes(ve + 1) & ~low_bytes(va);
-                        u[t].y &= low_bytes(ve - 3) & ~low_bytes(va - 4);
-                        u[t].z &= low_bytes(ve - 7) & ~low_bytes(va - 8);
-                        u[t].w &= low_bytes(ve - 11) & ~low_bytes(va - 12);
-                    }
+            for (int t = 0; t < kNt; ++t) {
+                uint4 x = *reinterpret_cast<const uint4*>(st + Sm::kKBytes + (kNt * g + t) * kBlk +
+                                                          (e4m3_chunk<64>(c, t) << 4));
+                if (edge) {
+                    x.x &= low_bytes(ve + 1) & ~low_bytes(va);
+                    x.y &= low_bytes(ve - 3) & ~low_bytes(va - 4);
+                    x.z &= low_bytes(ve - 7) & ~low_bytes(va - 8);
+                    x.w &= low_bytes(ve - 11) & ~low_bytes(va - 12);
                 }
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const uint32_t w[4] = {u[t].x, u[t].y, u[t].z, u[t].w};
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        mma_16816_f16(O[t0 + t], pa[s], e4m3_lo_to_f16x2(w[s]), e4m3_hi_to_f16x2(w[s]));
-                }
+                for (int s = 0; s < 4; ++s) mma_16816_f16(O[t], pa[s], e4m3_lo_to_f16x2(w[s]), e4m3_hi_to_f16x2(w[s]));
             }
         } else {
-            constexpr int kW = kVB / 4;                       // words of a value's run
-            uint32_t v[2][4][kW], vsf[2][4];
-            const int64_t tk = token(16 * c);
-            auto load_v = [&](int s) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint8_t* src = p.vc + (tk + 4 * s + k) * kRowB + g * kVB;
-                    if constexpr (kW == 4) {
-                        const uint4 u = __ldg(reinterpret_cast<const uint4*>(src));
-                        v[s & 1][k][0] = u.x;
-                        v[s & 1][k][1] = u.y;
-                        v[s & 1][k][kW - 2] = u.z;
-                        v[s & 1][k][kW - 1] = u.w;
-                    } else {
-                        const uint2 u = __ldg(reinterpret_cast<const uint2*>(src));
-                        v[s & 1][k][0] = u.x;
-                        v[s & 1][k][1] = u.y;
-                    }
-                    vsf[s & 1][k] = MX ? __ldg(p.vsf + (tk + 4 * s + k) * 4 + (g >> 1)) : 0u;
-                }
-            };
-            load_v(0);
+            constexpr int kW = kRow / 32;                     // words of a value's run
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                if (s < 3) load_v(s + 1);
+                uint32_t w[4][kW];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int o = 16 * s + 2 * c + (k & 1) + 8 * (k >> 1);
+                    const uint8_t* row = st + Sm::kKBytes + o * kRow;
+                    if constexpr (kW == 4) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(row + (e4m3_chunk<kRow>(g, o) << 4));
+                        w[k][0] = x.x;
+                        w[k][1] = x.y;
+                        w[k][kW - 2] = x.z;
+                        w[k][kW - 1] = x.w;
+                    } else {
+                        const uint2 x =
+                            *reinterpret_cast<const uint2*>(row + (e4m3_chunk<kRow>(g >> 1, o) << 4) + 8 * (g & 1));
+                        w[k][0] = x.x;
+                        w[k][1] = x.y;
+                    }
+                }
                 auto pair = [](float x, float y) { return MX ? bf16x2(x, y) : f16x2(x, y); };
                 const uint4 a = make_uint4(pair(S[2 * s][0], S[2 * s][1]), pair(S[2 * s][2], S[2 * s][3]),
                                            pair(S[2 * s + 1][0], S[2 * s + 1][1]),
                                            pair(S[2 * s + 1][2], S[2 * s + 1][3]));
-                auto& w = v[s & 1];
-                if (!MX && edge) {                            // (a NaN code times a weight of 0 is not 0)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (4 * s + k < va || 4 * s + k > ve) {
-#pragma unroll
-                            for (int x = 0; x < kW; ++x) w[k][x] = 0u;
-                        }
-                }
                 if constexpr (MX) {
                     // 16 channels of four keys: pairs (channel m, m + 4) of eight
                     // first, then the same channel of two keys side by side
                     uint32_t x[4][8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t E = min(vsf[s & 1][k], 252u);
+                        const uint32_t E = min((uint32_t) reinterpret_cast<const uint8_t*>(
+                            sc + kBlk)[4 * (16 * s + 2 * c + (k & 1) + 8 * (k >> 1)) + (g >> 1)], 252u);
                         const uint32_t e1 = E <= 128u ? E + 126u : 253u;
 #pragma unroll
                         for (int q = 0; q < 2; ++q) e2m1x8_to_bf16(w[k][q], (e1 << 7) | (e1 << 23), x[k] + 4 * q);
@@ -1570,16 +1670,28 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) rows_kernel(const RowsPara
                 }
             }
         }
+        __syncwarp();
+        if (more) {
+            copy(next, true);                                 // V's stage is free
+            landing |= 2;
+        } else {
+            cp_async_commit();
+        }
+        pg = next;
     }
-    // ---- the warp's (m, l, O), staged [channel][row]; the slices combined
-    __syncthreads();                                          // the query fragments are done with
+    // ---- the warp's (m, l, O), staged [channel][row] over its stage; the
+    // slices combined
+    cp_async_wait<0>();
+    if (landing & 1) mbar_wait_drain(&bar[0], phase[0]);      // (after a time-out alone)
+    if (landing & 2) mbar_wait_drain(&bar[1], phase[1]);
+    __syncwarp();
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
         if (c == 0) stat_s[warp][g + 8 * r] = make_float2(m[r], l[r]);
     }
-    float* os = o_s[warp];
+    float* os = reinterpret_cast<float*>(st);
     const float unit = MX || vexp == kNoExp ? 1.0f : pow2i(vexp);
 #pragma unroll
     for (int t = 0; t < kNt; ++t)
@@ -1589,33 +1701,30 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3) rows_kernel(const RowsPara
     const size_t part = (size_t)item * nsplit + split;
     float2* stat = (pre ? p.pre_stat : p.own_stat) + part * 64;
     float* out = (pre ? p.pre_o : p.own_o) + part * D * 64;
-    for (int r = tid; r < rows; r += 32 * kRowsWarps) {
-        float M = -INFINITY, ls = 0.0f;
-        for (int s = 0; s < slices; ++s) M = fmaxf(M, stat_s[(r >> 4) * slices + s][r & 15].x);
-        for (int s = 0; s < slices; ++s) {
-            const float2 x = stat_s[(r >> 4) * slices + s][r & 15];
-            if (x.x != -INFINITY) ls = fmaf(ex2_approx(x.x - M), x.y, ls);
-        }
-        stat[r] = make_float2(M, ls);
-    }
     // thread: row tid % 16 of an m-tile, channels tid / 16, + 8, ... (a part
     // without keys has no O)
-    for (int t = 0; t < (first < last ? mts : 0); ++t) {
-        const int r = tid & 15;
-        if (16 * t + r >= rows) continue;
-        float wt[kRowsWarps], M = -INFINITY;
-        for (int s = 0; s < slices; ++s) M = fmaxf(M, stat_s[t * slices + s][r].x);
+    const int r = tid & 15;
+    for (int t = 0; t < mts; ++t) {
+        const float2* ss = &stat_s[t << lg_slices][r];
+        float M = -INFINITY, ls = 0.0f;
+        for (int s = 0; s < slices; ++s) M = fmaxf(M, ss[16 * s].x);
+        float y[kNt];
 #pragma unroll
-        for (int s = 0; s < kRowsWarps; ++s) {
-            const float ms = s < slices ? stat_s[t * slices + s][r].x : -INFINITY;
-            wt[s] = ms == -INFINITY ? 0.0f : ex2_approx(ms - M);
+        for (int k = 0; k < kNt; ++k) y[k] = 0.0f;
+        for (int s = 0; s < slices; ++s) {
+            const float2 x = ss[16 * s];
+            const float wt = x.x == -INFINITY ? 0.0f : ex2_approx(x.x - M);
+            const float* o = reinterpret_cast<const float*>(sm + ((t << lg_slices) + s) * Sm::kStage) + (tid >> 4) * kPitch + r;
+            ls = fmaf(wt, x.y, ls);
+#pragma unroll
+            for (int k = 0; k < kNt; ++k) y[k] = fmaf(wt, o[8 * k * kPitch], y[k]);
         }
-        for (int d = tid >> 4; d < D; d += 2 * kRowsWarps) {
-            float y = 0.0f;
+        if (16 * t + r < rows) {
+            if (tid < 16) stat[16 * t + r] = make_float2(M, ls);
+            if (first < last) {
 #pragma unroll
-            for (int s = 0; s < kRowsWarps; ++s)
-                if (s < slices) y = fmaf(wt[s], o_s[t * slices + s][d * kPitch + r], y);
-            out[d * 64 + 16 * t + r] = y;
+                for (int k = 0; k < kNt; ++k) out[(8 * k + (tid >> 4)) * 64 + 16 * t + r] = y[k];
+            }
         }
     }
     if (p.late_wait) pdl_wait();                              // this grid ends after the one before it
@@ -1660,7 +1769,8 @@ SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
 }
 
 template <int D, bool MX, int RG>
-cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, cudaStream_t s) {
+cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, const CUtensorMap& tk, const CUtensorMap& tv,
+                          cudaStream_t s) {
     const DecodeArgs& a = sa.d;
     constexpr int kSmem = SmP<D, MX, RG>::kBytes + 1024;
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
@@ -1692,13 +1802,6 @@ cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, cudaS
     p.logit_scale_log2 = a.softmax_scale / static_cast<float>(D) * kLog2e;
     p.stat = reinterpret_cast<float2*>(ws + w.pre_stat);
     p.o = reinterpret_cast<float*>(ws + w.pre_o);
-    CUtensorMap tk, tv;
-    const bool ok = MX ? encode_cache_mx(&tk, a.k_cache, a.num_pages, a.Hk, a.page_size, D) &&
-                             encode_cache_mx(&tv, a.v_cache, a.num_pages, a.Hk, a.page_size, D)
-                       : encode_cache(&tk, a.k_cache, a.num_pages, a.Hk, a.page_size, D) &&
-                             (p.v_trans ? encode_cache_vt(&tv, a.v_cache, a.num_pages, a.Hk, D)
-                                        : encode_cache(&tv, a.v_cache, a.num_pages, a.Hk, a.page_size, D));
-    if (!ok) return cudaErrorInvalidValue;
     auto kern = prefix_kernel<D, MX, RG>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
@@ -1727,21 +1830,30 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     q.scale = reinterpret_cast<float*>(ws + w.q_scale);
     cudaError_t e = launch_pdl(query_kernel<D, MX>, dim3((unsigned)ceil_div(q.n_rows, 32), a.Hk), dim3(128), 0, s, q);
     if (e != cudaSuccess) return e;
+    // boxes of half a 128-token page; a transposed V also whole, for prefix_kernel
+    CUtensorMap tk, tv, tv128;
+    const bool vt = !MX && (a.kv_flags & 2);
+    const int box = std::min(a.page_size, kBlk);
+    const bool ok = MX ? encode_cache_mx(&tk, a.k_cache, a.num_pages, a.Hk, a.page_size, D, box) &&
+                             encode_cache_mx(&tv, a.v_cache, a.num_pages, a.Hk, a.page_size, D, box)
+                       : encode_cache(&tk, a.k_cache, a.num_pages, a.Hk, a.page_size, D, box) &&
+                             (vt ? encode_cache_vt(&tv, a.v_cache, a.num_pages, a.Hk, D, kBlk) &&
+                                       (few || encode_cache_vt(&tv128, a.v_cache, a.num_pages, a.Hk, D))
+                                 : encode_cache(&tv, a.v_cache, a.num_pages, a.Hk, a.page_size, D, box));
+    if (!ok) return cudaErrorInvalidValue;
     if (!few) {
-        e = w.pre_rows == 128 ? launch_prefix<D, MX, 1>(sa, w, s) : launch_prefix<D, MX, 2>(sa, w, s);
+        const CUtensorMap& tvp = vt ? tv128 : tv;
+        e = w.pre_rows == 128 ? launch_prefix<D, MX, 1>(sa, w, tk, tvp, s) : launch_prefix<D, MX, 2>(sa, w, tk, tvp, s);
         if (e != cudaSuccess) return e;
     }
     RowsParams r = {};
     r.q8 = q.codes;
     r.q_scale = q.scale;
-    r.kc = a.k_cache;
-    r.vc = a.v_cache;
     r.ksc = a.k_scale;
     r.vsc = a.v_scale;
     r.ksf = a.k_sf;
     r.vsf = a.v_sf;
     r.per_tensor = (a.kv_flags & 1) ? 1 : 0;
-    r.sc_vec = reinterpret_cast<uintptr_t>(a.k_scale) % 16 == 0 && reinterpret_cast<uintptr_t>(a.v_scale) % 16 == 0;
     r.ptab = a.page_table;
     r.prefix = sa.prefix_table;
     r.plen = sa.prefix_len;
@@ -1766,9 +1878,18 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     r.own_stat = reinterpret_cast<float2*>(ws + w.own_stat);
     r.own_o = reinterpret_cast<float*>(ws + w.own_o);
     r.late_wait = few ? 0 : 1;
+    r.div_np = fast_div_by(r.np);
+    r.div_ns = fast_div_by(r.ns);
+    r.div_hk = fast_div_by(r.Hk);
+    r.div_r = fast_div_by(r.R);
+    r.div_g = fast_div_by(r.G);
     const dim3 grid((unsigned)(r.np * a.Hk + (int64_t)w.ns * a.B * a.Hk)), block(32 * kRowsWarps);
-    if (!MX && (a.kv_flags & 2)) e = launch_pdl(rows_kernel<D, false, true>, grid, block, 0, s, r);
-    else e = launch_pdl(rows_kernel<D, MX, false>, grid, block, 0, s, r);
+    auto rows = [&](auto kern, int smem) {
+        const cudaError_t f = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return f != cudaSuccess ? f : launch_pdl(kern, grid, block, smem, s, tk, tv, r);
+    };
+    if (vt) e = rows(rows_kernel<D, false, true>, SmR<D, false, true>::kBytes + 1024);
+    else e = rows(rows_kernel<D, MX, false>, SmR<D, MX, false>::kBytes + 1024);
     if (e != cudaSuccess) return e;
     MergeParams m = {};
     m.pre_stat = r.pre_stat;
@@ -1782,7 +1903,7 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     m.pre_rows = w.pre_rows;
     m.n_rt = w.n_rt;
     m.unit = few ? kBlk : kKeys;
-    m.at_once = few ? kRowsWarps / (int)ceil_div(q.n_rows, 16) : kMinTiles;
+    m.lg_at_once = !few ? kLgMinTiles : (q.n_rows <= 16 ? 2 : (q.n_rows <= 32 ? 1 : 0));
     m.T = a.T;
     m.G = q.G;
     m.R = q.R;
