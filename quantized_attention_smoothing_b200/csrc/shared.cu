@@ -38,6 +38,7 @@ using namespace dec;
 __device__ unsigned g_shared_err;
 
 constexpr int kFewRows = 64;                 // rows that rows_kernel takes
+constexpr int kBlk = 64;                     // keys that a warp of it takes at a time
 
 // The splits, of at most nsplit, that n key tiles (prefix_kernel) or blocks
 // (rows_kernel) are shared out among: none gets fewer than a CTA works on at
@@ -122,55 +123,68 @@ struct MergeParams {
     const float2* own_stat;                  // [B Hk][ns][64]
     const float* own_o;                      // [B Hk][ns][D][64]
     const int32_t* plen;
-    int cap_prefix, np, ns, pre_rows, n_rt;
+    const int32_t* ctx;
+    int cap_prefix, cap_rows, window, np, ns, pre_rows, n_rt;
     int unit, lg_at_once;                    // keys of a tile or block of the prefix part, used_splits' third
+    int lg_own;                              // a sequence's own: used_splits' third
     int n_rows, R, T, G, Hk;
     __nv_bfloat16* out;
     int64_t os0, os1, os2, os3;
 };
 
+// Blocks [first, first + n) of a sequence's own keys, those of [L, ctx) that
+// one of its T query tokens sees, and the lowest and highest such key.
+__device__ __forceinline__ void own_keys(int ctx, int L, int T, int window, int& lo, int& hi, int& first, int& n) {
+    lo = max(L, ctx - T - window + 1);
+    hi = lo < ctx ? ctx - 1 : -1;
+    first = hi >= 0 ? lo / kBlk : 0;
+    n = hi >= 0 ? hi / kBlk + 1 - first : 0;
+}
+
 // CTA: 32 rows (lane = row: partials are channel-major, so a warp reads 128
-// contiguous bytes a channel) x kCh channels; its eight warps share out the
-// parts and are combined through shared memory.
+// contiguous bytes a channel) x kCh channels; its W warps share out the parts
+// and are combined through shared memory. A part's O is requested together
+// with its statistics, kAtOnce parts at a time, and dropped where the row has
+// no key in it (it then holds anything): with so few parts a warp, two
+// dependent trips to L2 were most of the time.
 constexpr int kCh = 16;
 
-template <int D>
-__global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) {
-    __shared__ float2 st[8][32];
-    __shared__ float acc_s[8][kCh][33];
+template <int D, int W>
+__global__ void __launch_bounds__(32 * W) shared_merge_kernel(const MergeParams p) {
+    __shared__ float2 st[W][32];
+    __shared__ float acc_s[W][kCh][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int d0 = blockIdx.y * kCh, hk = blockIdx.z;
     const int n = blockIdx.x * 32 + lane;
-    const bool in = n < p.n_rows;
-    const int nn = in ? n : p.n_rows - 1;
-    const int b = nn / p.R, rr = nn % p.R;
-    const int L = max(0, min(*p.plen, p.cap_prefix));
+    const int nn = min(n, p.n_rows - 1);
+    const int b = nn / p.R, rr = nn - b * p.R;
+    const int rt = nn / p.pre_rows, r = nn - rt * p.pre_rows;
+    pdl_wait();
+    const int ctx = max(0, min(__ldg(p.ctx + b), p.cap_rows));
+    const int L = max(0, min(__ldg(p.plen), p.cap_prefix));
     const int np = L > 0 ? used_splits((L + p.unit - 1) / p.unit, p.np, p.lg_at_once) : 0;
-    const size_t part_p = ((size_t)hk * p.n_rt + nn / p.pre_rows) * p.np, part_o = ((size_t)b * p.Hk + hk) * p.ns;
-    const int r = nn % p.pre_rows;
+    int lo, hi, first, n_own;
+    own_keys(ctx, L, p.T, p.window, lo, hi, first, n_own);
+    const int parts = np + (n_own > 0 ? used_splits(n_own, p.ns, p.lg_own) : 0);
+    const int most = __reduce_max_sync(0xffffffffu, parts);
+    const size_t part_p = ((size_t)hk * p.n_rt + rt) * p.np, part_o = ((size_t)b * p.Hk + hk) * p.ns;
     float M = -INFINITY, l = 0.0f, acc[kCh];
 #pragma unroll
     for (int k = 0; k < kCh; ++k) acc[k] = 0.0f;
-    // kAtOnce parts at a time: their statistics, then the O of those that have keys
     constexpr int kAtOnce = 4;
-    for (int e0 = warp; e0 < np + p.ns; e0 += 8 * kAtOnce) {
+    for (int e0 = warp; e0 < most; e0 += W * kAtOnce) {
         float2 s[kAtOnce];
         float v[kAtOnce][kCh];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-            const int e = e0 + 8 * i;
+            const int e = e0 + W * i;
             s[i] = make_float2(-INFINITY, 0.0f);
-            if (e < np) s[i] = __ldcg(p.pre_stat + (part_p + e) * p.pre_rows + r);
-            else if (e < np + p.ns) s[i] = __ldcg(p.own_stat + (part_o + e - np) * 64 + rr);
-        }
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const int e = e0 + 8 * i;
-            const bool pre = e < np;
-            const int rows = pre ? p.pre_rows : 64;
-            const float* o = pre ? p.pre_o + ((part_p + e) * D + d0) * rows + r
-                                 : p.own_o + ((part_o + e - np) * D + d0) * rows + rr;
-            if (s[i].x != -INFINITY) {
+            if (e < parts) {
+                const bool pre = e < np;
+                const int rows = pre ? p.pre_rows : 64, row = pre ? r : rr;
+                const size_t part = pre ? part_p + e : part_o + e - np;
+                s[i] = __ldcg((pre ? p.pre_stat : p.own_stat) + part * rows + row);
+                const float* o = (pre ? p.pre_o : p.own_o) + (part * D + d0) * rows + row;
 #pragma unroll
                 for (int k = 0; k < kCh; ++k) v[i][k] = __ldcg(o + k * rows);
             }
@@ -190,9 +204,9 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) 
     __syncthreads();
     float Mt = -INFINITY, lt = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) Mt = fmaxf(Mt, st[w][lane].x);
+    for (int w = 0; w < W; ++w) Mt = fmaxf(Mt, st[w][lane].x);
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
+    for (int w = 0; w < W; ++w) {
         const float2 s = st[w][lane];
         if (s.x != -INFINITY) lt = fmaf(ex2_approx(s.x - Mt), s.y, lt);
     }
@@ -201,19 +215,22 @@ __global__ void __launch_bounds__(256) shared_merge_kernel(const MergeParams p) 
     for (int k = 0; k < kCh; ++k) acc_s[warp][k][lane] = acc[k] * scale;
     __syncthreads();
     // thread: row, two channels
-    const int row = threadIdx.x >> 3, c2 = 2 * (threadIdx.x & 7);
-    const int n2 = blockIdx.x * 32 + row;
-    if (n2 >= p.n_rows) return;
-    float y0 = 0.0f, y1 = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-        y0 += acc_s[w][c2][row];
-        y1 += acc_s[w][c2 + 1][row];
+    for (int i = 0; i < 8 / W; ++i) {
+        const int row = (threadIdx.x >> 3) + 4 * W * i, c2 = 2 * (threadIdx.x & 7);
+        const int n2 = blockIdx.x * 32 + row;
+        if (n2 >= p.n_rows) return;
+        float y0 = 0.0f, y1 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            y0 += acc_s[w][c2][row];
+            y1 += acc_s[w][c2 + 1][row];
+        }
+        const int b2 = n2 / p.R, r2 = n2 % p.R, t = r2 / p.G, h = hk * p.G + r2 % p.G;
+        __nv_bfloat16* dst = p.out + b2 * p.os0 + t * p.os1 + h * p.os2 + (int64_t)(d0 + c2) * p.os3;
+        dst[0] = __float2bfloat16_rn(y0);
+        dst[p.os3] = __float2bfloat16_rn(y1);
     }
-    const int b2 = n2 / p.R, r2 = n2 % p.R, t = r2 / p.G, h = hk * p.G + r2 % p.G;
-    __nv_bfloat16* dst = p.out + b2 * p.os0 + t * p.os1 + h * p.os2 + (int64_t)(d0 + c2) * p.os3;
-    dst[0] = __float2bfloat16_rn(y0);
-    dst[p.os3] = __float2bfloat16_rn(y1);
 }
 
 // ------------------------------------------------------------------ prefix
@@ -1158,8 +1175,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 //              D g / 8 .., one per n-tile, converted exactly in registers.
 // With the boxes' swizzles these reads take every bank once, those of a
 // 64-byte V row (V^T) twice.
-constexpr int kBlk = 64;                     // keys a warp takes at a time
 constexpr int kRowsWarps = 4;
+
+// log2 of the key slices that its four warps make with this many rows
+__host__ __device__ inline int lg_slices(int rows) { return rows <= 16 ? 2 : (rows <= 32 ? 1 : 0); }
 
 struct RowsParams {
     const uint8_t* q8;                       // [Hk][rows_pad][D] e4m3 codes
@@ -1269,8 +1288,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
     const int rows = pre ? p.n_rows : p.R;
     const int n0 = b * p.R;                                   // first row (pre: b = 0)
     // warps: m-tile (16 rows) x key slice
-    const int mts = (rows + 15) >> 4, lg_slices = mts == 1 ? 2 : (mts == 2 ? 1 : 0), slices = 1 << lg_slices;
-    const int mt = warp >> lg_slices, slice = warp & (slices - 1);
+    const int mts = (rows + 15) >> 4, lg_s = lg_slices(rows), slices = 1 << lg_s;
+    const int mt = warp >> lg_s, slice = warp & (slices - 1);
     const bool live = mt < mts;
     // everything the set-up reads, requested together
     int L = *p.plen;
@@ -1318,7 +1337,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
     }
     // [lo, hi]: keys that any row sees (a sequence's T rows see all of its keys
     // from the first one's window on)
-    int lo, hi;
+    int lo, hi, blk0, n_all;
     if (pre) {
         if (tid == 0) {
             span[0] = INT32_MAX;
@@ -1334,16 +1353,23 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
         __syncthreads();
         lo = span[0];
         hi = span[1];
+        blk0 = hi >= 0 ? lo / kBlk : 0;
+        n_all = hi >= 0 ? hi / kBlk + 1 - blk0 : 0;
     } else {
-        const int x = max(0, min(ctx[0], cap));
-        lo = max(max(L, 0), x - p.T - p.window + 1);
-        hi = lo < x ? x - 1 : -1;
+        own_keys(max(0, min(ctx[0], cap)), L, p.T, p.window, lo, hi, blk0, n_all);
     }
-    const int blk0 = hi >= 0 ? lo / kBlk : 0, n_all = hi >= 0 ? hi / kBlk + 1 - blk0 : 0;
     int first, last;
-    share_out(n_all, used_splits(n_all, nsplit, lg_slices), split, first, last);
+    share_out(n_all, used_splits(n_all, nsplit, lg_s), split, first, last);
     first += blk0;
     last += blk0;
+    const size_t part = (size_t)item * nsplit + split;
+    float2* stat = (pre ? p.pre_stat : p.own_stat) + part * 64;
+    float* out = (pre ? p.pre_o : p.own_o) + part * D * 64;
+    if (first >= last) {                                      // (most CTAs of a short call)
+        if (tid < rows) stat[tid] = make_float2(-INFINITY, 0.0f);
+        if (p.late_wait) pdl_wait();
+        return;
+    }
 
     const int32_t* tab = pre ? p.prefix : p.ptab + (int64_t)b * p.max_pages;
     const int lgp = min(p.lg_page, 6);                        // keys of one page inside a block (log2)
@@ -1698,14 +1724,10 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
 #pragma unroll
         for (int e = 0; e < 4; ++e) os[(kNt * (2 * c + (e & 1)) + t) * kPitch + g + 8 * (e >> 1)] = O[t][e] * unit;
     __syncthreads();
-    const size_t part = (size_t)item * nsplit + split;
-    float2* stat = (pre ? p.pre_stat : p.own_stat) + part * 64;
-    float* out = (pre ? p.pre_o : p.own_o) + part * D * 64;
-    // thread: row tid % 16 of an m-tile, channels tid / 16, + 8, ... (a part
-    // without keys has no O)
+    // thread: row tid % 16 of an m-tile, channels tid / 16, + 8, ...
     const int r = tid & 15;
     for (int t = 0; t < mts; ++t) {
-        const float2* ss = &stat_s[t << lg_slices][r];
+        const float2* ss = &stat_s[t << lg_s][r];
         float M = -INFINITY, ls = 0.0f;
         for (int s = 0; s < slices; ++s) M = fmaxf(M, ss[16 * s].x);
         float y[kNt];
@@ -1714,17 +1736,15 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
         for (int s = 0; s < slices; ++s) {
             const float2 x = ss[16 * s];
             const float wt = x.x == -INFINITY ? 0.0f : ex2_approx(x.x - M);
-            const float* o = reinterpret_cast<const float*>(sm + ((t << lg_slices) + s) * Sm::kStage) + (tid >> 4) * kPitch + r;
+            const float* o = reinterpret_cast<const float*>(sm + ((t << lg_s) + s) * Sm::kStage) + (tid >> 4) * kPitch + r;
             ls = fmaf(wt, x.y, ls);
 #pragma unroll
             for (int k = 0; k < kNt; ++k) y[k] = fmaf(wt, o[8 * k * kPitch], y[k]);
         }
         if (16 * t + r < rows) {
             if (tid < 16) stat[16 * t + r] = make_float2(M, ls);
-            if (first < last) {
 #pragma unroll
-                for (int k = 0; k < kNt; ++k) out[(8 * k + (tid >> 4)) * 64 + 16 * t + r] = y[k];
-            }
+            for (int k = 0; k < kNt; ++k) out[(8 * k + (tid >> 4)) * 64 + 16 * t + r] = y[k];
         }
     }
     if (p.late_wait) pdl_wait();                              // this grid ends after the one before it
@@ -1811,8 +1831,12 @@ cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, const
 template <int D, bool MX>
 cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     const DecodeArgs& a = sa.d;
-    const SharedPlan w = shared_plan(a.B, a.T, a.H, a.Hk, D);
+    SharedPlan w = shared_plan(a.B, a.T, a.H, a.Hk, D);
     const bool few = w.pre_rows == kFewRows;
+    // no more splits than the tables have room for
+    w.np = used_splits((int)ceil_div((int64_t)sa.max_prefix_pages * a.page_size, few ? kBlk : kKeys), w.np,
+                       few ? lg_slices(a.B * a.T * (a.H / a.Hk)) : kLgMinTiles);
+    w.ns = used_splits((int)ceil_div((int64_t)a.max_pages * a.page_size, kBlk), w.ns, lg_slices(a.T * (a.H / a.Hk)));
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     QueryParams q = {};
     q.q = static_cast<const uint16_t*>(a.q.ptr);
@@ -1903,7 +1927,7 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     m.pre_rows = w.pre_rows;
     m.n_rt = w.n_rt;
     m.unit = few ? kBlk : kKeys;
-    m.lg_at_once = !few ? kLgMinTiles : (q.n_rows <= 16 ? 2 : (q.n_rows <= 32 ? 1 : 0));
+    m.lg_at_once = few ? lg_slices(q.n_rows) : kLgMinTiles;
     m.T = a.T;
     m.G = q.G;
     m.R = q.R;
@@ -1914,9 +1938,14 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     m.os1 = a.out_stride[1];
     m.os2 = a.out_stride[2];
     m.os3 = a.out_stride[3];
-    // a plain stream-ordered launch: it starts after both parts
-    shared_merge_kernel<D><<<dim3((unsigned)ceil_div(m.n_rows, 32), D / kCh, a.Hk), 256, 0, s>>>(m);
-    return cudaGetLastError();
+    m.ctx = a.ctx_lens;
+    m.cap_rows = a.max_pages * a.page_size;
+    m.window = r.window;
+    m.lg_own = lg_slices(q.R);
+    // (four warps hold all of sixteen parts at once)
+    const dim3 mg((unsigned)ceil_div(m.n_rows, 32), D / kCh, a.Hk);
+    return w.np + w.ns <= 16 ? launch_pdl(shared_merge_kernel<D, 4>, mg, dim3(128), 0, s, m)
+                             : launch_pdl(shared_merge_kernel<D, 8>, mg, dim3(256), 0, s, m);
 }
 
 }  // namespace
