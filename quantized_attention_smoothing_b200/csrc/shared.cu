@@ -1148,8 +1148,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // all rows against the prefix. With 16 rows a key costs 4 D FLOPs a byte of
 // cache, far from what a tensor pipe is bound by; what counts is latency and
 // bytes in flight. So no TMEM and no roles: a warp takes 16 rows and 64 keys
-// at a time through mma fragments (FP8: QK on the e4m3 codes, PV on fp16;
-// MXFP4: both on bf16), and three CTAs of four independent warps share an SM.
+// at a time through mma fragments (FP8: fp16, MXFP4: bf16, both exact), and
+// two or three CTAs of four independent warps share an SM.
 // One lane copies a warp's blocks (a TMA box of K or V per page, scales by
 // cp.async): the next block's K is on its way while this one's softmax and PV
 // run, the next V while the next QK runs, one stage of each being enough.
@@ -1205,20 +1205,21 @@ struct RowsParams {
 
 template <int D, bool MX, bool VT>
 struct SmR {
-    static constexpr int kSteps = MX ? D / 16 : D / 32;              // QK steps
+    static constexpr int kSteps = D / 16;                            // QK steps
     static constexpr int kRow = MX ? D / 2 : D;                      // bytes of a cache row
     static constexpr int kPitch = 17;                                // rows of a staged O
     static constexpr int kKBytes = kBlk * kRow, kVBytes = VT ? D * kBlk : kBlk * kRow;
     // a warp's K and V, later its O; then all warps' scales [k | v][64]
     static constexpr int kStage = al1024(kKBytes + kVBytes > D * kPitch * 4 ? kKBytes + kVBytes : D * kPitch * 4);
     static constexpr int kScale = kRowsWarps * kStage;
-    static constexpr int kQf = kScale + kRowsWarps * 2 * 4 * kBlk;   // MX: [m-tile][step][lane] query fragments
-    static constexpr int kStat = kQf + (MX ? 4 * kSteps * 32 * 16 : 0);
+    static constexpr int kStat = kScale + kRowsWarps * 2 * 4 * kBlk;
     static constexpr int kSpan = kStat + kRowsWarps * 16 * 8;        // lowest, highest key any row sees
     static constexpr int kBar = kSpan + 8;                           // [warp][k | v], then [warp] abort flags
-    static constexpr int kBytes = kBar + kRowsWarps * 16 + kRowsWarps * 4;
+    static constexpr int kQf = (kBar + kRowsWarps * 20 + 15) & ~15;  // [m-tile][step][lane] query fragments
+    // with m-tiles of 16 rows; three CTAs an SM with one, two with more
+    static constexpr int bytes(int mts) { return 1024 + kQf + mts * kSteps * 32 * 16; }
     static_assert(kKBytes % 1024 == 0 && kBar % 8 == 0, "alignment");
-    static_assert(3 * (kBytes + 2048) <= 228 * 1024, "three CTAs an SM");
+    static_assert(3 * (bytes(1) + 1024) <= 228 * 1024 && 2 * (bytes(4) + 1024) <= 228 * 1024, "CTAs an SM");
 };
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
@@ -1230,13 +1231,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint4& a, uint32_
 
 __device__ __forceinline__ void mma_16816_f16(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_16832_e4m3(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
@@ -1432,34 +1426,35 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
         copy(pg, true);
         landing = 3;
     }
-    // the query codes as A fragments, thread (g, c) holding the run c D / 4 ..
-    // of rows g and g + 8: e4m3 as they are; for an MXFP4 cache their exact
-    // bf16 values, pairs (m, m + 4) of eight channels as e2m1_block_to_bf16
-    // orders K's, in shared memory
-    uint4 qa[MX ? 1 : kSteps];
-    {
+    // the query codes as A fragments in shared memory, thread (g, c) holding the
+    // run c D / 4 .. of rows g and g + 8: their exact fp16 values (an e4m3
+    // mma.sync is made of conversions and fp16 products on this machine, the
+    // queries' anew for every key tile); for an MXFP4 cache bf16, pairs
+    // (m, m + 4) of eight channels as e2m1_block_to_bf16 orders K's
+    if (live && slice == 0) {
         const uint32_t* w0 = reinterpret_cast<const uint32_t*>(u[0]);
         const uint32_t* w1 = reinterpret_cast<const uint32_t*>(u[1]);
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
+            uint4 a;
             if constexpr (MX) {
                 const int k = s & ~1;
-                uint4 a;
                 if ((s & 1) == 0)
                     a = make_uint4(e4m3_pick_to_bf16x2<0>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<0>(w1[k], w1[k + 1]),
                                    e4m3_pick_to_bf16x2<1>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<1>(w1[k], w1[k + 1]));
                 else
                     a = make_uint4(e4m3_pick_to_bf16x2<2>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<2>(w1[k], w1[k + 1]),
                                    e4m3_pick_to_bf16x2<3>(w0[k], w0[k + 1]), e4m3_pick_to_bf16x2<3>(w1[k], w1[k + 1]));
-                if (live && slice == 0) qf[(mt * kSteps + s) * 32 + lane] = a;
             } else {
-                qa[s] = make_uint4(w0[2 * s], w1[2 * s], w0[2 * s + 1], w1[2 * s + 1]);
+                a = make_uint4(e4m3_lo_to_f16x2(w0[s]), e4m3_lo_to_f16x2(w1[s]), e4m3_hi_to_f16x2(w0[s]),
+                               e4m3_hi_to_f16x2(w1[s]));
             }
+            qf[(mt * kSteps + s) * 32 + lane] = a;
         }
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) cq[r] = fmaxf(cq[r] * p.logit_scale_log2, FLT_MIN);
-    if (MX) __syncthreads();
+    __syncthreads();
 
     // key (of the block) of element x of this thread's pair in n-tile j
     auto key_of = [&](int j, int x) { return VT ? 16 * c + 2 * j + x : 8 * j + 2 * c + x; };
@@ -1481,25 +1476,37 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
         landed(0);
         if (!ok) break;
         float S[8][4];
+        constexpr int kAt = MX ? 2 : 4, kRun = MX ? 1 : D / 64;        // n-tiles at a time; 16-byte runs of a key
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int o = VT ? 16 * (g >> 1) + 2 * j + (g & 1) : 8 * j + g;
-            uint4 kr[MX ? 1 : D / 64];
+        for (int j0 = 0; j0 < 8; j0 += kAt) {
+            uint32_t kb[kAt][MX ? 16 : 4 * kRun];
 #pragma unroll
-            for (int k = 0; k < (MX ? 1 : D / 64); ++k)
-                kr[k] = *reinterpret_cast<const uint4*>(st + o * kRow + (e4m3_chunk<kRow>((MX ? 1 : D / 64) * c + k, o) << 4));
+            for (int j = 0; j < kAt; ++j) {
+                const int o = VT ? 16 * (g >> 1) + 2 * (j0 + j) + (g & 1) : 8 * (j0 + j) + g;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) S[j][e] = 0.0f;
-            if constexpr (MX) {
-                uint32_t kb[16];
-                e2m1_block_to_bf16(kr[0], reinterpret_cast<const uint8_t*>(sc)[4 * o + c], kb);
+                for (int k = 0; k < kRun; ++k) {
+                    const uint4 x =
+                        *reinterpret_cast<const uint4*>(st + o * kRow + (e4m3_chunk<kRow>(kRun * c + k, o) << 4));
+                    if constexpr (MX) {
+                        e2m1_block_to_bf16(x, reinterpret_cast<const uint8_t*>(sc)[4 * o + c], kb[j]);
+                    } else {
+                        kb[j][4 * k] = x.x;
+                        kb[j][4 * k + 1] = x.y;
+                        kb[j][4 * k + 2] = x.z;
+                        kb[j][4 * k + 3] = x.w;
+                    }
+                }
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-                    mma_16816(S[j], qf[(mt * kSteps + s) * 32 + lane], kb[2 * s], kb[2 * s + 1]);
-            } else {
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(kr);
+                for (int e = 0; e < 4; ++e) S[j0 + j][e] = 0.0f;
+            }
 #pragma unroll
-                for (int s = 0; s < kSteps; ++s) mma_16832_e4m3(S[j], qa[s], w[2 * s], w[2 * s + 1]);
+            for (int s = 0; s < kSteps; ++s) {
+                const uint4 a = qf[(mt * kSteps + s) * 32 + lane];
+#pragma unroll
+                for (int j = 0; j < kAt; ++j) {
+                    if constexpr (MX) mma_16816(S[j0 + j], a, kb[j][2 * s], kb[j][2 * s + 1]);
+                    else mma_16816_f16(S[j0 + j], a, e4m3_lo_to_f16x2(kb[j][s]), e4m3_hi_to_f16x2(kb[j][s]));
+                }
             }
         }
         // ---- scales of keys 16 c .., masks, maxima
@@ -1764,10 +1771,10 @@ SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
     const int64_t rows = (int64_t)B * T * (H / Hk), sms = device_sms();
     w.pre_rows = rows <= kFewRows ? kFewRows : (rows <= 256 ? 128 : 256);
     w.n_rt = (int)ceil_div(rows, w.pre_rows);
-    // one CTA an SM for prefix_kernel, three for rows_kernel
+    // one CTA an SM for prefix_kernel, two or three for rows_kernel
     const bool few = w.pre_rows == kFewRows;
     w.np = (int)std::max<int64_t>(1, (few ? 2 * sms : sms) / ((int64_t)w.n_rt * Hk));
-    w.ns = (int)std::max<int64_t>(1, std::min<int64_t>(32, (few ? 1 : 3) * sms / ((int64_t)B * Hk)));
+    w.ns = (int)std::max<int64_t>(1, std::min<int64_t>(32, (few ? 1 : (T * (H / Hk) > 16 ? 2 : 3)) * sms / ((int64_t)B * Hk)));
     w.rows_pad = few ? (int)rows : w.n_rt * w.pre_rows;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -1908,12 +1915,13 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     r.div_r = fast_div_by(r.R);
     r.div_g = fast_div_by(r.G);
     const dim3 grid((unsigned)(r.np * a.Hk + (int64_t)w.ns * a.B * a.Hk)), block(32 * kRowsWarps);
+    const int mts = (int)ceil_div(few ? q.n_rows : q.R, 16);
     auto rows = [&](auto kern, int smem) {
         const cudaError_t f = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         return f != cudaSuccess ? f : launch_pdl(kern, grid, block, smem, s, tk, tv, r);
     };
-    if (vt) e = rows(rows_kernel<D, false, true>, SmR<D, false, true>::kBytes + 1024);
-    else e = rows(rows_kernel<D, MX, false>, SmR<D, MX, false>::kBytes + 1024);
+    if (vt) e = rows(rows_kernel<D, false, true>, SmR<D, false, true>::bytes(mts));
+    else e = rows(rows_kernel<D, MX, false>, SmR<D, MX, false>::bytes(mts));
     if (e != cudaSuccess) return e;
     MergeParams m = {};
     m.pre_stat = r.pre_stat;
