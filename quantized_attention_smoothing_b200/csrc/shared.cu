@@ -73,6 +73,12 @@ __device__ __forceinline__ uint32_t f16x2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // 2^e for |e| <= 252 (two normal factors, so that no half of it underflows).
 __device__ __forceinline__ float pow2i(int e) {
     const int a = e / 2, b = e - a;
@@ -97,9 +103,10 @@ __device__ __forceinline__ uint32_t low_bytes(int n) {
 }
 
 // An FP8 cache's value scales are taken relative to a power of two, 2^e, so
-// that the weights p v_scale 2^-e fit fp16 (they keep 11 bits down to 2^-14;
-// bf16 would keep 8): e is the exponent of the first tile's largest scale and
-// is raised when a later tile has one over 2^kScaleRoom times as large, O
+// that what they are multiplied into fits fp16 (which keeps 11 bits where bf16
+// would keep 8): the converted V rows of prefix_kernel, the weights of
+// rows_kernel. e is the exponent of the first tile's largest scale and is
+// raised when a later tile has one over 2^kScaleRoom times as large, O
 // following by an exact power of two. Slots that hold no key of the part
 // count as zero, whatever they hold.
 constexpr int kScaleRoom = 4;
@@ -115,13 +122,18 @@ __device__ __forceinline__ int scale_exp(int e, float vmax) {
 // weights hold as exactly as values below one, and most tiles leave O alone.
 constexpr float kLazyMax = 8.0f;
 
+// Partials are laid out [D / 4][rows][4 channels] fp32: a warp whose lanes are
+// rows writes and reads 512 contiguous bytes with one 16-byte access a lane
+// (channel by channel, 128 bytes at a time, the 128 KB of a prefix CTA took
+// 5000 cycles to leave it).
+
 // ------------------------------------------------------------------- merge
 
 struct MergeParams {
     const float2* pre_stat;                  // [Hk n_rt][np][pre_rows]
-    const float* pre_o;                      // [Hk n_rt][np][D][pre_rows]
+    const float* pre_o;                      // [Hk n_rt][np][D / 4][pre_rows][4]
     const float2* own_stat;                  // [B Hk][ns][64]
-    const float* own_o;                      // [B Hk][ns][D][64]
+    const float* own_o;                      // [B Hk][ns][D / 4][64][4]
     const int32_t* plen;
     const int32_t* ctx;
     int cap_prefix, cap_rows, window, np, ns, pre_rows, n_rt;
@@ -141,8 +153,7 @@ __device__ __forceinline__ void own_keys(int ctx, int L, int T, int window, int&
     n = hi >= 0 ? hi / kBlk + 1 - first : 0;
 }
 
-// CTA: 32 rows (lane = row: partials are channel-major, so a warp reads 128
-// contiguous bytes a channel) x kCh channels; its W warps share out the parts
+// CTA: 32 rows (lane = row) x kCh channels; its W warps share out the parts
 // and are combined through shared memory. A part's O is requested together
 // with its statistics, kAtOnce parts at a time, and dropped where the row has
 // no key in it (it then holds anything): with so few parts a warp, two
@@ -184,9 +195,15 @@ __global__ void __launch_bounds__(32 * W) shared_merge_kernel(const MergeParams 
                 const int rows = pre ? p.pre_rows : 64, row = pre ? r : rr;
                 const size_t part = pre ? part_p + e : part_o + e - np;
                 s[i] = __ldcg((pre ? p.pre_stat : p.own_stat) + part * rows + row);
-                const float* o = (pre ? p.pre_o : p.own_o) + (part * D + d0) * rows + row;
+                const float4* o = reinterpret_cast<const float4*>(pre ? p.pre_o : p.own_o) + (part * (D / 4) + d0 / 4) * rows + row;
 #pragma unroll
-                for (int k = 0; k < kCh; ++k) v[i][k] = __ldcg(o + k * rows);
+                for (int k = 0; k < kCh / 4; ++k) {
+                    const float4 x = __ldcg(o + k * rows);
+                    v[i][4 * k] = x.x;
+                    v[i][4 * k + 1] = x.y;
+                    v[i][4 * k + 2] = x.z;
+                    v[i][4 * k + 3] = x.w;
+                }
             }
         }
 #pragma unroll
@@ -367,9 +384,11 @@ constexpr int kConvWarp0 = 8, kTmaWarp = 12, kMmaWarp0 = 13, kScaleWarp = 14, kM
 // 256 x 168 + 128 x 96 + 128 x 80 <= 512 x 128 registers, the launch's own
 constexpr int kRegsSoft = 168, kRegsConv = 96, kRegsProd = 80;
 static_assert(256 * kRegsSoft + 128 * kRegsConv + 128 * kRegsProd <= kThreads * 128, "register split");
-// A row's first maximum further below its starting point than this is taken as
-// the running max before any weight is computed (p would lose bits, or vanish).
-constexpr float kFarMax = 60.0f;
+// A unit's 64 weights against the running max: where they add up to more than
+// kMaxSum some logit is over 2 above it, and the max is raised wherever that is
+// so (kRaise); where a row's first ones add up to less than kMinSum they have
+// lost bits, or vanished, and its max is taken first.
+constexpr float kMaxSum = 256.0f, kRaise = 2.0f, kMinSum = 0x1p-54f;
 // one pair of exponentials in 2 kPolyEvery goes to the FMA pipe
 constexpr int kPolyEvery = 4;
 
@@ -384,10 +403,11 @@ struct PrefixParams {
     const int32_t* ptab;
     const int32_t* plen;
     const int32_t* ctx;
-    int T, Hk, G, R, n_rows, page, lg_page, cap_prefix, cap_rows, num_pages, window, np, n_rt;
+    FastDiv div_r, div_g;
+    int T, Hk, R, n_rows, page, lg_page, cap_prefix, cap_rows, num_pages, window, np, n_rt;
     float logit_scale_log2;
     float2* stat;                            // [Hk n_rt][np][128 RG]
-    float* o;                                // [Hk n_rt][np][D][128 RG]
+    float* o;                                // [Hk n_rt][np][D / 4][128 RG][4]
 };
 
 template <int D, bool MX, int RG>
@@ -407,8 +427,8 @@ struct SmP {
     static constexpr int kKbBuf = MX ? kKeys * 2 * D : 0;
     static constexpr int kVb = kKb + kKbBuf;                         // [2] bf16 V, D / 64 atoms [128][128 B]
     static constexpr int kVbBuf = kKeys * 2 * D;
-    static constexpr int kScale = kVb + 2 * kVbBuf;                  // [slot][k | v][128] fp32
-    static constexpr int kScSlot = MX ? 0 : 2 * kKeys;
+    static constexpr int kScale = kVb + 2 * kVbBuf;                  // [slot] k [128] fp32, v [128] fp16
+    static constexpr int kScSlot = MX ? 0 : kKeys + kKeys / 2;
     static constexpr int kMeta = kScale + kScStages * kScSlot * 4;   // [slot] bad-page mask; exponent of the value scales
     static constexpr int kSpan = kMeta + 2 * kScStages * 4;              // [8 warps] lowest, highest key any row sees
     static constexpr int kBar = kSpan + 2 * 8 * 4;
@@ -498,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (i >= Sm::kPReady && i < Sm::kPReady + 4) cnt = 4;                      // softmax group
             if (i >= Sm::kVReady && i < Sm::kVReady + 2) cnt = 4;                      // converters
             if (i >= Sm::kScFull && i < Sm::kScFull + kScStages) cnt = 32;
-            if (i >= Sm::kScEmpty && i < Sm::kScEmpty + kScStages) cnt = 4 * RG;       // the groups that read the tile
+            if (i >= Sm::kScEmpty && i < Sm::kScEmpty + kScStages) cnt = 4 * RG + (MX ? 0 : 4);   // softmax groups, converters
             if (i >= Sm::kKbReady && i < Sm::kKbReady + 2) cnt = 4;
             if (i >= Sm::kVFree && i < Sm::kVFree + 2) cnt = RG;                       // the groups' PV commits
             if (i == Sm::kKbFree) cnt = RG;                                            // their QK commits
@@ -518,20 +538,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
 
+    // what the set-up reads, requested together: the length, and the softmax
+    // thread's row
     int L = *p.plen;
-    if (L > p.cap_prefix || L < 0) {
-        if (tid == 0 && split == 0) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
-        L = max(0, min(L, p.cap_prefix));
-    }
-    // the softmax thread's row, and the keys of the prefix that it sees
     const int g = (warp >> 2) & 1;
     const int r = RG == 2 ? (tid & 255) : (tid & 127);
     const int n = row0 + r;
     const bool rv = n < p.n_rows;
+    int ctx = 0;
+    float q_scale = 0.0f;
+    if (warp < 8 && rv) {
+        ctx = __ldg(p.ctx + fast_div(n, p.div_r));
+        q_scale = __ldcg(p.q_scale + (size_t)blockIdx.y * kRowsCta + r);
+    }
+    const float ks_t = !MX && p.per_tensor ? __ldg(p.ksc) : 1.0f, vs_t = !MX && p.per_tensor ? __ldg(p.vsc) : 1.0f;
+    if (L > p.cap_prefix || L < 0) {
+        if (tid == 0 && split == 0) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
+        L = max(0, min(L, p.cap_prefix));
+    }
+    // the keys of the prefix that the row sees
     int key_lo = INT32_MAX, key_hi = -1;
     if (warp < 8 && rv) {
-        const int ctx = max(0, min(__ldg(p.ctx + n / p.R), p.cap_rows));
-        const int pq = ctx - p.T + (n % p.R) / p.G;
+        const int pq = max(0, min(ctx, p.cap_rows)) - p.T + fast_div(n - fast_div(n, p.div_r) * p.R, p.div_g);
         key_lo = max(0, pq - p.window + 1);
         key_hi = min(pq, L - 1);
         if (key_hi < key_lo) {
@@ -573,8 +601,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (as decode.cu's: lane j of chunk c looks up page 32 c + j of the
         // CTA's pages; a page that holds no key below L is not looked up)
         const bool kv = warp == kTmaWarp;
-        const float ks_t = !MX && !kv && p.per_tensor ? __ldg(p.ksc) : 1.0f;
-        const float vs_t = !MX && !kv && p.per_tensor ? __ldg(p.vsc) : 1.0f;
         int chunk = -1, phys = 0, issued = 0, vexp = kNoExp;
         bool bad = false, found = false;
         if (kv && lane == 0 && nt > 0) {
@@ -635,26 +661,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 const unsigned badm = __ballot_sync(0xffffffffu, mine && bad) >> slot0;
                 if (lane == 0) meta[c] = static_cast<int>(badm);
-                if constexpr (MX) {
+                if (MX || p.per_tensor) {
+                    if (lane == 0) meta[kScStages + c] = 0;
                     mbar_arrive(&bars[Sm::kScFull + c]);
                 } else {
                     // keys 4 lane .. 4 lane + 3: k_scale, and v_scale relative to
                     // 2^vexp, zero where the slot holds no key of the prefix
                     float ks[4], vs[4];
-                    if (p.per_tensor) {
+                    const int pq = __shfl_sync(0xffffffffu, phys, slot0 + 4 * lane / p.page);
+                    const int64_t src = ((int64_t)pq * p.Hk + hk) * p.page + (4 * lane) % p.page;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            ks[e] = ks_t;
-                            vs[e] = vs_t;
-                        }
-                    } else {
-                        const int pq = __shfl_sync(0xffffffffu, phys, slot0 + 4 * lane / p.page);
-                        const int64_t src = ((int64_t)pq * p.Hk + hk) * p.page + (4 * lane) % p.page;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            ks[e] = __ldg(p.ksc + src + e);
-                            vs[e] = __ldg(p.vsc + src + e);
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        ks[e] = __ldg(p.ksc + src + e);
+                        vs[e] = __ldg(p.vsc + src + e);
                     }
                     const int key = (tb + i) * kKeys + 4 * lane;
                     const bool off_page = (badm >> (4 * lane / p.page)) & 1;
@@ -669,8 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float f = vexp == kNoExp ? 0.0f : pow2i(-vexp);
                     float* dst = scl + c * Sm::kScSlot + 4 * lane;
                     *reinterpret_cast<float4*>(dst) = make_float4(ks[0], ks[1], ks[2], ks[3]);
-                    *reinterpret_cast<float4*>(dst + kKeys) =
-                        make_float4(vs[0] * f, vs[1] * f, vs[2] * f, vs[3] * f);
+                    *reinterpret_cast<uint2*>(scl + c * Sm::kScSlot + kKeys + 2 * lane) =
+                        make_uint2(f16x2(vs[0] * f, vs[1] * f), f16x2(vs[2] * f, vs[3] * f));
                     if (lane == 0) meta[kScStages + c] = vexp;
                     mbar_arrive(&bars[Sm::kScFull + c]);
                 }
@@ -788,11 +807,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       reg_alloc<kRegsSoft>();
         // ------------------------------------------------------------ softmax
         // base-2 logit = (S k_scale) cq; cq >= FLT_MIN keeps a masked -inf
-        const float cq = fmaxf(rv ? __ldcg(p.q_scale + (size_t)blockIdx.y * kRowsCta + r) * p.logit_scale_log2 : 0.0f, FLT_MIN);
+        const float cq = fmaxf(q_scale * p.logit_scale_log2 * ks_t, FLT_MIN);
         const uint64_t cq2 = f2_pack(cq, cq);
         const uint32_t trow = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
         const uint32_t to = trow + kOCol + 128 * g;
         const bool idle = __all_sync(0xffffffffu, !rv);      // 32 rows of padding: the warp only keeps time
+        const bool tensor = MX || p.per_tensor;              // logits without a scale of their own
         // A row starts from m = 0, which holds for its first maximum too unless
         // that is far off; l = 0 says that it has seen no key.
         float m_run = 0.0f;
@@ -804,20 +824,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int h = k & 1, i = RG == 2 ? k >> 1 : 2 * (k >> 1) + g, c = i % kScStages;
             const uint32_t ts = trow + 64 * (2 * g + h);
             ok = warp_all(mbar_wait(&bars[Sm::kSFull + 2 * g + h], (k >> 1) & 1, abort_flag, &g_shared_err, 8));
-            if (ok && h == 0)
-                ok = warp_all(mbar_wait(&bars[Sm::kScFull + c], (i / kScStages) & 1, abort_flag, &g_shared_err, 9));
             if (!ok) break;
-            if (!idle) {
+            uint32_t x0[32], x1[32];
+            if (h == 0) ok = warp_all(mbar_wait(&bars[Sm::kScFull + c], (i / kScStages) & 1, abort_flag, &g_shared_err, 9));
+            if (!idle) {                                     // (on its way during what comes up to the wait below)
                 tc_fence_after();
+                tmem_ld32(ts, x0);
+                tmem_ld32(ts + 32, x1);
+            }
+            if (!idle) {
                 const int key0 = (tb + i) * kKeys + 64 * h;
                 const int badm = meta[c];
                 const float4* ks = reinterpret_cast<const float4*>(scl + c * Sm::kScSlot + 64 * h);
-                const float4* vs = ks + kKeys / 4;
                 // y = S k_scale of keys 4 q .. 4 q + 3 of 32 loaded columns
-                auto scaled = [&](const uint32_t (&x)[32], int cc, int q, uint64_t& y01, uint64_t& y23) {
+                auto scaled = [&](bool plain, const uint32_t (&x)[32], int cc, int q, uint64_t& y01, uint64_t& y23) {
                     y01 = f2_pack(__uint_as_float(x[4 * q]), __uint_as_float(x[4 * q + 1]));
                     y23 = f2_pack(__uint_as_float(x[4 * q + 2]), __uint_as_float(x[4 * q + 3]));
-                    if constexpr (!MX) {
+                    if (!plain) {
                         const float4 s = ks[8 * cc + q];
                         y01 = f2_mul(y01, f2_pack(s.x, s.y));
                         y23 = f2_mul(y23, f2_pack(s.z, s.w));
@@ -825,11 +848,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 // two words of P from the logits' base-2 exponents; l += p (a
                 // masked key's exponent is -inf, which only MUFU makes exactly 0)
-                auto weigh = [&](auto masked, uint64_t e01, uint64_t e23, int cc, int q, uint64_t& l, uint32_t* w) {
+                auto weigh = [&](auto masked, uint64_t e01, uint64_t e23, int q, uint64_t& l, uint32_t* w) {
                     float a, b, p0, p1, p2, p3;
                     f2_unpack(e01, a, b);
                     if (!decltype(masked)::value && q % kPolyEvery == kPolyEvery - 1) {
-                        exp2_poly_x2(a, b, p0, p1);
+                        exp2_poly_x2(fminf(a, 127.0f), fminf(b, 127.0f), p0, p1);
                     } else {
                         p0 = ex2_approx(a);
                         p1 = ex2_approx(b);
@@ -837,57 +860,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                     f2_unpack(e23, a, b);
                     p2 = ex2_approx(a);
                     p3 = ex2_approx(b);
-                    uint64_t p01 = f2_pack(p0, p1), p23 = f2_pack(p2, p3);
-                    l = f2_add(l, f2_add(p01, p23));
-                    if constexpr (!MX) {
-                        const float4 v = vs[8 * cc + q];
-                        p01 = f2_mul(p01, f2_pack(v.x, v.y));
-                        p23 = f2_mul(p23, f2_pack(v.z, v.w));
-                    }
-                    f2_unpack(p01, p0, p1);
-                    f2_unpack(p23, p2, p3);
+                    l = f2_add(l, f2_add(f2_pack(p0, p1), f2_pack(p2, p3)));
                     w[2 * q] = MX ? bf16x2(p0, p1) : f16x2(p0, p1);
                     w[2 * q + 1] = MX ? bf16x2(p2, p3) : f16x2(p2, p3);
                 };
-                uint32_t x0[32], x1[32];
-                tmem_ld32(ts, x0);
-                tmem_ld32(ts + 32, x1);
-                tmem_wait_ld(x0);
-                tmem_wait_ld(x1);
-                // Most units are inside every row's window and raise no row's
-                // maximum by much, so their weights are computed against the
-                // running one while the unit's own is still being found: one
-                // pass in which loads, FMA and MUFU overlap. Where the unit
-                // turns out to need more, nothing of the pass is kept.
+                // Most units are wholly seen, or not at all, by every row and
+                // raise no row's maximum by much, so their weights are computed
+                // against the running one, and their sum tells whether that was
+                // right: no weight is above 2^8 where 64 of them add up to no
+                // more. Where the unit turns out to need its own maximum,
+                // nothing of the pass is kept.
                 const int ve = MX ? 0 : meta[kScStages + c];
                 if (vexp == kNoExp) vexp = ve;               // (no key before: O holds zeros)
-                bool slow = ve != vexp || !__all_sync(0xffffffffu, !rv || (key0 >= key_lo && key0 + 63 <= key_hi && badm == 0));
-                if (!slow) {
+                const bool none = key_hi < key0 || key_lo > key0 + 63, all = key_lo <= key0 && key_hi >= key0 + 63;
+                bool slow = ve != vexp || badm != 0 || key0 + 63 >= L || !__all_sync(0xffffffffu, none || all);
+                tmem_wait_ld(x0);
+                tmem_wait_ld(x1);
+                if (!ok) break;
+                auto fast = [&](auto plain) {
                     const uint64_t nsub2 = f2_pack(-m_run, -m_run);
-                    uint64_t l = l2;
-                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    uint64_t lu[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
                     uint32_t w[2][16];
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
                             uint64_t y01, y23;
-                            scaled(cc == 0 ? x0 : x1, cc, q, y01, y23);
-                            float a, b;
-                            f2_unpack(y01, a, b);
-                            m4[2 * (q & 1)] = fmax3(m4[2 * (q & 1)], a, b);
-                            f2_unpack(y23, a, b);
-                            m4[2 * (q & 1) + 1] = fmax3(m4[2 * (q & 1) + 1], a, b);
-                            weigh(std::false_type{}, f2_fma(y01, cq2, nsub2), f2_fma(y23, cq2, nsub2), cc, q, l, w[cc]);
+                            scaled(decltype(plain)::value, cc == 0 ? x0 : x1, cc, q, y01, y23);
+                            weigh(std::false_type{}, f2_fma(y01, cq2, nsub2), f2_fma(y23, cq2, nsub2), q, lu[q & 1], w[cc]);
                         }
                     }
-                    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * cq;
-                    slow = __any_sync(0xffffffffu, rv && (mx > m_run + kLazyMax || (l2 == 0 && mx < m_run - kFarMax)));
+                    const uint64_t lsum = f2_add(lu[0], lu[1]);
+                    float a, b;
+                    f2_unpack(lsum, a, b);
+                    a += b;
+                    slow = __any_sync(0xffffffffu, all && (a > kMaxSum || (l2 == 0 && a < kMinSum)));
                     if (!slow) {
-                        l2 = l;
+                        if (__any_sync(0xffffffffu, none)) {
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) w[q / 16][q % 16] = none ? 0u : w[q / 16][q % 16];
+                        }
+                        if (!none) l2 = f2_add(l2, lsum);
                         tmem_st16(ts, w[0]);
                         tmem_st16(ts + 16, w[1]);
                     }
+                };
+                if (!slow) {
+                    if (tensor) fast(std::true_type{});
+                    else fast(std::false_type{});
                 }
                 if (slow) {
                     const int clo = key_lo - key0, chi = key_hi - key0;
@@ -900,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_wait_ld(x);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            scaled(x, cc, q, y[16 * cc + 2 * q], y[16 * cc + 2 * q + 1]);
+                            scaled(tensor, x, cc, q, y[16 * cc + 2 * q], y[16 * cc + 2 * q + 1]);
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const int j = 32 * cc + 4 * q + 2 * e;
@@ -918,7 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float alpha = 1.0f;
                     if (l2 == 0) {
                         if (mx > -INFINITY) m_run = mx;       // its first key (O is zero)
-                    } else if (mx > m_run + kLazyMax) {
+                    } else if (mx > m_run + kRaise) {
                         alpha = ex2_approx(m_run - mx);
                         l2 = f2_mul(l2, f2_pack(alpha, alpha));
                         m_run = mx;
@@ -951,13 +971,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             weigh(std::true_type{}, f2_fma(y[16 * cc + 2 * q], cq2, nsub2),
-                                  f2_fma(y[16 * cc + 2 * q + 1], cq2, nsub2), cc, q, l2, w);
+                                  f2_fma(y[16 * cc + 2 * q + 1], cq2, nsub2), q, l2, w);
                         tmem_st16(ts + 16 * cc, w);
                     }
                 }
                 tmem_wait_st();
                 tc_fence_before();
             }
+            if (!ok) break;
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&bars[Sm::kPReady + 2 * g + h]);
@@ -974,11 +995,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             m_run = -INFINITY;
             l = 0.0f;
         }
-        const float unit = MX || vexp == kNoExp ? 1.0f : pow2i(vexp);
+        const float unit = MX || vexp == kNoExp ? 1.0f : vs_t * pow2i(vexp);
         tc_fence_after();
-        // channel of TMEM column j (MX: the order of the converted V rows)
-        auto chan = [](int j) { return MX ? (j & ~7) + ((j >> 1) & 3) + 4 * (j & 1) : j; };
-        float* po = p.o + part * D * kRowsCta + r;
+        // four channels, of columns j .. of O (MX: the eight columns of a group
+        // hold channels 0 4 1 5 2 6 3 7)
+        float4* po = reinterpret_cast<float4*>(p.o) + part * (D / 4) * kRowsCta + r;
+        auto put = [&](int col, const float (&y)[32]) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+                po[(col + j) / 4 * kRowsCta] = MX ? make_float4(y[j], y[j + 2], y[j + 4], y[j + 6])
+                                                  : make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+                po[((col + j) / 4 + 1) * kRowsCta] = MX ? make_float4(y[j + 1], y[j + 3], y[j + 5], y[j + 7])
+                                                        : make_float4(y[j + 4], y[j + 5], y[j + 6], y[j + 7]);
+            }
+        };
         if constexpr (RG == 2) {
             p.stat[part * kRowsCta + r] = make_float2(m_run, l);
             if (my_units > 0 && !idle) {
@@ -987,8 +1017,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t o[32];
                     tmem_ld32(to + 32 * hf, o);
                     tmem_wait_ld(o);
+                    float y[32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) po[chan(32 * hf + j) * kRowsCta] = __uint_as_float(o[j]) * unit;
+                    for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(o[j]) * unit;
+                    put(32 * hf, y);
                 }
             }
             tc_fence_before();
@@ -1023,14 +1055,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t o[32];
                     tmem_ld32(to + keep + 32 * hf, o);
                     tmem_wait_ld(o);
+                    float y[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        const int col = keep + 32 * hf + j;
                         // (a group without a key in the row has no O)
-                        float y = m_run == -INFINITY ? 0.0f : wa * unit * __uint_as_float(o[j]);
-                        if (other.x != -INFINITY) y = fmaf(wb, xo[col * 128 + r], y);
-                        po[chan(col) * 128] = y;
+                        y[j] = m_run == -INFINITY ? 0.0f : wa * unit * __uint_as_float(o[j]);
+                        if (other.x != -INFINITY) y[j] = fmaf(wb, xo[(keep + 32 * hf + j) * 128 + r], y[j]);
                     }
+                    put(keep + 32 * hf, y);
                 }
             }
             tc_fence_before();
@@ -1084,9 +1116,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 // 16-byte chunk c of the code row (V: 16 channels of a key;
                 // V^T: 16 keys of a channel) -> two chunks of the fp16 row;
-                // slots behind the prefix's end count as zeros
+                // slots behind the prefix's end count as zeros, the others'
+                // scales (relative to 2^vexp, rounded to fp16) are multiplied in
+                const int c8 = i % kScStages;
+                if (!warp_all(mbar_wait(&bars[Sm::kScFull + c8], (i / kScStages) & 1, abort_flag, &g_shared_err, 16))) break;
+                const uint8_t* vsc = reinterpret_cast<const uint8_t*>(scl + c8 * Sm::kScSlot + kKeys);
+                const uint32_t vs_row = p.per_tensor || p.v_trans
+                                            ? 0u : 0x10001u * *reinterpret_cast<const uint16_t*>(vsc + 2 * row);
                 const int left = L - (tb + i) * kKeys;           // keys of the tile below L
-                auto convert = [&](auto width_c, int atom_b) {
+                auto convert = [&](auto width_c, auto trans_c, int atom_b) {
+                    constexpr bool kTrans = decltype(trans_c)::value;
                     constexpr int kWidth = decltype(width_c)::value;
                     const uint8_t* vrow = sm + Sm::kV + s * Sm::kKStage + row * kWidth;
                     uint4 u[kWidth / 16];
@@ -1096,7 +1135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (left < kKeys) {
 #pragma unroll
                         for (int c = 0; c < kWidth / 16; ++c) {
-                            const int n = p.v_trans ? left - 16 * c : (row < left ? 16 : 0);
+                            const int n = kTrans ? left - 16 * c : (row < left ? 16 : 0);
                             u[c].x &= low_bytes(n);
                             u[c].y &= low_bytes(n - 4);
                             u[c].z &= low_bytes(n - 8);
@@ -1107,18 +1146,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int c = 0; c < kWidth / 16; ++c) {
                         uint8_t* at = dst + (c >> 2) * atom_b;
                         const int ch = 2 * (c & 3);
-                        *reinterpret_cast<uint4*>(at + ((ch ^ (row & 7)) << 4)) =
-                            make_uint4(e4m3_lo_to_f16x2(u[c].x), e4m3_hi_to_f16x2(u[c].x), e4m3_lo_to_f16x2(u[c].y),
-                                       e4m3_hi_to_f16x2(u[c].y));
-                        *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (row & 7)) << 4)) =
-                            make_uint4(e4m3_lo_to_f16x2(u[c].z), e4m3_hi_to_f16x2(u[c].z), e4m3_lo_to_f16x2(u[c].w),
-                                       e4m3_hi_to_f16x2(u[c].w));
+                        uint32_t f[8] = {e4m3_lo_to_f16x2(u[c].x), e4m3_hi_to_f16x2(u[c].x), e4m3_lo_to_f16x2(u[c].y),
+                                         e4m3_hi_to_f16x2(u[c].y), e4m3_lo_to_f16x2(u[c].z), e4m3_hi_to_f16x2(u[c].z),
+                                         e4m3_lo_to_f16x2(u[c].w), e4m3_hi_to_f16x2(u[c].w)};
+                        if (!p.per_tensor) {
+                            uint32_t v8[8];
+                            if (kTrans) {
+                                const uint4 a = *reinterpret_cast<const uint4*>(vsc + 32 * c);
+                                const uint4 b = *reinterpret_cast<const uint4*>(vsc + 32 * c + 16);
+                                v8[0] = a.x, v8[1] = a.y, v8[2] = a.z, v8[3] = a.w;
+                                v8[4] = b.x, v8[5] = b.y, v8[6] = b.z, v8[7] = b.w;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[e] = f16x2_mul(f[e], kTrans ? v8[e] : vs_row);
+                        }
+                        *reinterpret_cast<uint4*>(at + ((ch ^ (row & 7)) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<uint4*>(at + (((ch + 1) ^ (row & 7)) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
                     }
                 };
                 if (p.v_trans) {
-                    if (row < D) convert(std::integral_constant<int, kKeys>{}, D * 128);
+                    if (row < D) convert(std::integral_constant<int, kKeys>{}, std::true_type{}, D * 128);
                 } else {
-                    convert(std::integral_constant<int, D>{}, kKeys * 128);
+                    convert(std::integral_constant<int, D>{}, std::false_type{}, kKeys * 128);
                 }
             }
             fence_proxy_async_smem();
@@ -1126,6 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 mbar_arrive(&bars[Sm::kVReady + vb]);
                 mbar_arrive(&bars[Sm::kKvEmpty + s]);
+                if (!MX) mbar_arrive(&bars[Sm::kScEmpty + i % kScStages]);
             }
         }
     }
@@ -1197,7 +1247,7 @@ struct RowsParams {
     FastDiv div_np, div_ns, div_hk, div_r, div_g;
     float logit_scale_log2;
     float2* pre_stat;                        // [Hk][np][64]
-    float* pre_o;                            // [Hk][np][D][64]
+    float* pre_o;                            // [Hk][np][D / 4][64][4]
     float2* own_stat;                        // [B Hk][ns][64]
     float* own_o;
     int late_wait;                           // launched behind prefix_kernel, of which it reads nothing
@@ -1731,7 +1781,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
 #pragma unroll
         for (int e = 0; e < 4; ++e) os[(kNt * (2 * c + (e & 1)) + t) * kPitch + g + 8 * (e >> 1)] = O[t][e] * unit;
     __syncthreads();
-    // thread: row tid % 16 of an m-tile, channels tid / 16, + 8, ...
+    // thread: row tid % 16 of an m-tile, channels 4 (tid / 16 + 8 i) ..
     const int r = tid & 15;
     for (int t = 0; t < mts; ++t) {
         const float2* ss = &stat_s[t << lg_s][r];
@@ -1743,15 +1793,17 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
         for (int s = 0; s < slices; ++s) {
             const float2 x = ss[16 * s];
             const float wt = x.x == -INFINITY ? 0.0f : ex2_approx(x.x - M);
-            const float* o = reinterpret_cast<const float*>(sm + ((t << lg_s) + s) * Sm::kStage) + (tid >> 4) * kPitch + r;
+            const float* o = reinterpret_cast<const float*>(sm + ((t << lg_s) + s) * Sm::kStage) + (tid >> 4) * 4 * kPitch + r;
             ls = fmaf(wt, x.y, ls);
 #pragma unroll
-            for (int k = 0; k < kNt; ++k) y[k] = fmaf(wt, o[8 * k * kPitch], y[k]);
+            for (int k = 0; k < kNt; ++k) y[k] = fmaf(wt, o[(32 * (k >> 2) + (k & 3)) * kPitch], y[k]);
         }
         if (16 * t + r < rows) {
             if (tid < 16) stat[16 * t + r] = make_float2(M, ls);
 #pragma unroll
-            for (int k = 0; k < kNt; ++k) out[(8 * k + (tid >> 4)) * 64 + 16 * t + r] = y[k];
+            for (int k = 0; k < kNt; k += 4)
+                reinterpret_cast<float4*>(out)[(2 * k + (tid >> 4)) * 64 + 16 * t + r] =
+                    make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
         }
     }
     if (p.late_wait) pdl_wait();                              // this grid ends after the one before it
@@ -1815,8 +1867,9 @@ cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, const
     p.ctx = a.ctx_lens;
     p.T = a.T;
     p.Hk = a.Hk;
-    p.G = a.H / a.Hk;
-    p.R = a.T * p.G;
+    p.R = a.T * (a.H / a.Hk);
+    p.div_r = fast_div_by(p.R);
+    p.div_g = fast_div_by(a.H / a.Hk);
     p.n_rows = a.B * p.R;
     p.page = a.page_size;
     p.lg_page = 31 - __builtin_clz(static_cast<unsigned>(a.page_size));
