@@ -163,7 +163,7 @@ sage_status append_args(sage_hadamard h, const sage_cview4& k, const sage_cview4
     if (!sizes_ok(size, k.stride) || !sizes_ok(size, v.stride)) return SAGE_ERR_INVALID_ARG;
     if (k.size[0] != 1 || k.size[3] != h->D) return SAGE_ERR_INVALID_ARG;
     if (!page_ok(page_size)) return SAGE_ERR_UNSUPPORTED;
-    if (size[1] * size[2] * (h->D / 32) >= (int64_t(1) << 31) || (int64_t)num_pages * page_size >= (int64_t(1) << 31) ||
+    if (size[1] * size[2] * (h->D / 16) >= (int64_t(1) << 31) || (int64_t)num_pages * page_size >= (int64_t(1) << 31) ||
         (int64_t)num_pages * size[2] * page_size * h->D >= (int64_t(1) << 40))
         return SAGE_ERR_UNSUPPORTED;
     if (!aligned(k.ptr, 2) || !aligned(v.ptr, 2) || !aligned(k_mean, 16) || !aligned(slot_map, 4) ||
