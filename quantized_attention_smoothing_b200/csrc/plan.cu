@@ -308,8 +308,7 @@ cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t s) {
     p.prefix_pages = a.prefix_pages;
     p.inline_slots = a.max_tokens <= kInlineTokens ? 1 : 0;
     const size_t smem = (4 * (size_t)a.B + 3) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (4 * kPlanMaxRows + 3) * (int)sizeof(int));
+    cudaError_t e = allow_smem<plan_kernel>((4 * kPlanMaxRows + 3) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
     // one CTA for every 1024 slots, rows and (as a guess) table entries
     const int64_t items = (p.inline_slots ? a.max_tokens : kInlineTokens) + (int64_t)a.B;

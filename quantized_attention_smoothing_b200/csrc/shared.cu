@@ -19,6 +19,7 @@
 // row groups of a CTA keep it busy in turn.
 #include <algorithm>
 #include <cfloat>
+#include <cmath>
 #include <cstdint>
 #include <type_traits>
 
@@ -378,7 +379,6 @@ __global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
 // waiting for both products: 1800 of 5500 cycles a unit spent waiting, and 128
 // logits a thread spilled; 120 us against 62 us for 4096 rows x 32768 keys.)
 constexpr int kScStages = 8;                 // scale ring
-constexpr int kLgMinTiles = 1;               // two key tiles: what a CTA has in flight
 constexpr int kThreads = 512;
 constexpr int kConvWarp0 = 8, kTmaWarp = 12, kMmaWarp0 = 13, kScaleWarp = 14, kMmaWarp1 = 15;
 // 256 x 168 + 128 x 96 + 128 x 80 <= 512 x 128 registers, the launch's own
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t0 = hi >= 0 ? lo / kKeys : 0;
     const int n_all = hi >= 0 ? hi / kKeys + 1 - t0 : 0;
     int tb, te;
-    share_out(n_all, used_splits(n_all, p.np, kLgMinTiles), split, tb, te);
+    share_out(n_all, used_splits(n_all, p.np, RG == 1 ? 1 : 0), split, tb, te);
     const int nt = te - tb;
     tb += t0;
     const int ppt = kKeys / p.page;
@@ -1818,15 +1818,17 @@ struct SharedPlan {
     size_t pre_stat, pre_o, own_stat, own_o, codes, img, q_scale, bytes;
 };
 
+// The most that a batch of these sizes may be cut into, whatever its lengths,
+// and the layout that has room for it.
 SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
     SharedPlan w;
-    const int64_t rows = (int64_t)B * T * (H / Hk), sms = device_sms();
-    w.pre_rows = rows <= kFewRows ? kFewRows : (rows <= 256 ? 128 : 256);
+    const int64_t rows = (int64_t)B * T * (H / Hk), sms = device_sms(), items = (int64_t)B * Hk;
+    const bool few = rows <= kFewRows;
+    w.pre_rows = few ? kFewRows : (rows <= 128 ? 128 : 256);
     w.n_rt = (int)ceil_div(rows, w.pre_rows);
     // one CTA an SM for prefix_kernel, two or three for rows_kernel
-    const bool few = w.pre_rows == kFewRows;
     w.np = (int)std::max<int64_t>(1, (few ? 2 * sms : sms) / ((int64_t)w.n_rt * Hk));
-    w.ns = (int)std::max<int64_t>(1, std::min<int64_t>(32, (few ? 1 : (T * (H / Hk) > 16 ? 2 : 3)) * sms / ((int64_t)B * Hk)));
+    w.ns = (int)std::max<int64_t>(1, std::min<int64_t>(32, (few ? 1 : (T * (H / Hk) > 16 ? 2 : 3)) * sms / items));
     w.rows_pad = few ? (int)rows : w.n_rt * w.pre_rows;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -1834,7 +1836,9 @@ SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
         at += (n + 255) & ~(size_t)255;
         return o;
     };
-    const size_t pre = (size_t)w.n_rt * Hk * w.np * w.pre_rows, own = (size_t)B * Hk * w.ns * 64;
+    // (in 128-row CTAs no more than in 256-row ones: at most one an SM, or one
+    // a row tile)
+    const size_t pre = std::max<size_t>((size_t)w.n_rt * Hk * w.np, few ? 0 : sms) * w.pre_rows, own = (size_t)items * w.ns * 64;
     const size_t q_rows = (size_t)Hk * w.rows_pad;
     w.pre_stat = take(pre * sizeof(float2));
     w.own_stat = take(own * sizeof(float2));
@@ -1845,6 +1849,70 @@ SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
     w.q_scale = take(q_rows * sizeof(float));
     w.bytes = at;
     return w;
+}
+
+// The cut of a call, by its estimated time. A prefix CTA has an SM to itself;
+// the sequences' own CTAs run on the SMs left over, or behind it, and 128 or
+// 256 rows a CTA trade partials for conversions of V, so the most CTAs are not
+// the least time: MXFP4 B32 behind 16384 tokens takes 37.8 us with 128 prefix
+// CTAs of two tiles and 27.9 us with 86 of three, B16 T4 window 4096 36.8 and
+// 30.6. The model's constants (microseconds; tiles are 128 keys, blocks 64
+// keys a warp) are fitted to 44 batches of 65 to 4096 rows over all their cuts:
+// its choice is 1.5 % slower than the best one on average, 10 % at worst. The
+// lengths are on the device; the tables' sizes stand for them, and a sequence's
+// own keys for half of what its table has room for (only the time depends on
+// that).
+void choose_cut(const DecodeSharedArgs& sa, SharedPlan& w) {
+    const DecodeArgs& a = sa.d;
+    const int sms = device_sms(), R = a.T * (a.H / a.Hk), lg_s = lg_slices(R), per_sm = R > 16 ? 2 : 3;
+    const int64_t rows = (int64_t)a.B * R, items = (int64_t)a.B * a.Hk;
+    const int64_t cap_pre = (int64_t)sa.max_prefix_pages * a.page_size, cap_row = (int64_t)a.max_pages * a.page_size;
+    const int64_t seen = std::min<int64_t>(cap_row, (int64_t)a.window + a.T);
+    if (w.pre_rows == kFewRows) {
+        w.np = used_splits((int)ceil_div(cap_pre, kBlk), w.np, lg_slices((int)rows));
+        w.ns = used_splits((int)ceil_div(cap_row, kBlk), w.ns, lg_s);
+        return;
+    }
+    const int tiles = (int)std::max<int64_t>(1, std::min(ceil_div(cap_pre, kKeys), ceil_div(seen, kKeys) + 1));
+    const int blocks = (int)ceil_div(std::max<int64_t>(kBlk, std::min(cap_row - cap_pre + a.page_size, seen)), kBlk);
+    const int half = std::max(1, blocks / 2);                              // of an average sequence
+    const float pre_fixed[3] = {0.0f, 5.3f, 6.3f}, tile[3] = {0.0f, a.mx ? 2.3f : 1.45f, a.mx ? 3.6f : 2.75f};
+    const float own_fixed = 5.4f, own_block = a.mx ? 4.0f : 2.0f;
+    const float beside = 0.6f, merge_bytes = 6.9e6f;                       // share of the SMs left over; bytes a us
+    const SharedPlan most = w;
+    float best = FLT_MAX;
+    for (int rg = rows <= 128 ? 1 : 2; rg >= 1; --rg) {
+        const int64_t units = ceil_div(rows, 128 * rg) * a.Hk;            // row tiles of all heads
+        if (rg == 1 && most.pre_rows == 256 && units > sms) continue;      // (the layout's bound)
+        const int np_max = (int)std::max<int64_t>(1, sms / units), step = rg == 1 ? 2 : 1;
+        int per = (int)ceil_div(std::max(ceil_div(tiles, np_max), (int64_t)step), step) * step;
+        for (int n = 0; n < 7; ++n, per += std::max(step, per / 4 / step * step)) {
+            const int np = (int)ceil_div(tiles, per);
+            const float ctas = (float)units * np, tp = pre_fixed[rg] + per * tile[rg];
+            const float waves = std::ceil(ctas / sms), slots = std::max(0.0f, sms - ctas) * per_sm * beside;
+            for (int ns = 1;; ns = std::min(2 * ns, most.ns)) {
+                const int used = std::max(1, std::min(ns, (half + (1 << lg_s) - 1) >> lg_s));
+                const int least = std::min(ns, used_splits(blocks, ns, lg_s));
+                const float most_own = own_fixed + own_block * ceil_div(blocks, (int64_t)least << lg_s);
+                const float mean_own = own_fixed + own_block * ceil_div(half, (int64_t)used << lg_s);
+                const float work = (float)items * used * mean_own, rest = work - slots * tp;
+                float t = std::max(waves * tp, most_own);
+                if (ctas >= sms) t = waves * tp + std::max(work / (sms * per_sm), most_own);
+                else if (rest > 0.0f) t = std::max(tp + std::max(rest / (sms * per_sm), mean_own), most_own);
+                t += (ctas * 128 * rg + (float)items * used * R) * a.D * 4 / merge_bytes;
+                if (t < best) {
+                    best = t;
+                    w.pre_rows = 128 * rg;
+                    w.n_rt = (int)(units / a.Hk);
+                    w.np = np;
+                    w.ns = ns;
+                    w.rows_pad = w.n_rt * w.pre_rows;
+                }
+                if (ns == most.ns) break;
+            }
+            if (np == 1) break;
+        }
+    }
 }
 
 template <int D, bool MX, int RG>
@@ -1882,21 +1950,24 @@ cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, const
     p.logit_scale_log2 = a.softmax_scale / static_cast<float>(D) * kLog2e;
     p.stat = reinterpret_cast<float2*>(ws + w.pre_stat);
     p.o = reinterpret_cast<float*>(ws + w.pre_o);
-    auto kern = prefix_kernel<D, MX, RG>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const cudaError_t e = allow_smem<prefix_kernel<D, MX, RG>>(kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(w.np, w.n_rt * a.Hk), dim3(kThreads), kSmem, s, tk, tv, p);
+    return launch_pdl(prefix_kernel<D, MX, RG>, dim3(w.np, w.n_rt * a.Hk), dim3(kThreads), kSmem, s, tk, tv, p);
 }
 
 template <int D, bool MX>
 cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     const DecodeArgs& a = sa.d;
-    SharedPlan w = shared_plan(a.B, a.T, a.H, a.Hk, D);
+    // (a function of the sizes alone: a serving loop's next call has the same)
+    const int sizes[] = {device_sms(), a.B, a.T, a.H, a.Hk, a.page_size, a.max_pages, a.window, sa.max_prefix_pages};
+    static thread_local int last[9] = {};
+    static thread_local SharedPlan w;
+    if (!std::equal(sizes, sizes + 9, last)) {
+        w = shared_plan(a.B, a.T, a.H, a.Hk, D);
+        choose_cut(sa, w);
+        std::copy(sizes, sizes + 9, last);
+    }
     const bool few = w.pre_rows == kFewRows;
-    // no more splits than the tables have room for
-    w.np = used_splits((int)ceil_div((int64_t)sa.max_prefix_pages * a.page_size, few ? kBlk : kKeys), w.np,
-                       few ? lg_slices(a.B * a.T * (a.H / a.Hk)) : kLgMinTiles);
-    w.ns = used_splits((int)ceil_div((int64_t)a.max_pages * a.page_size, kBlk), w.ns, lg_slices(a.T * (a.H / a.Hk)));
     uint8_t* ws = static_cast<uint8_t*>(a.ws);
     QueryParams q = {};
     q.q = static_cast<const uint16_t*>(a.q.ptr);
@@ -1969,12 +2040,15 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     r.div_g = fast_div_by(r.G);
     const dim3 grid((unsigned)(r.np * a.Hk + (int64_t)w.ns * a.B * a.Hk)), block(32 * kRowsWarps);
     const int mts = (int)ceil_div(few ? q.n_rows : q.R, 16);
-    auto rows = [&](auto kern, int smem) {
-        const cudaError_t f = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        return f != cudaSuccess ? f : launch_pdl(kern, grid, block, smem, s, tk, tv, r);
-    };
-    if (vt) e = rows(rows_kernel<D, false, true>, SmR<D, false, true>::bytes(mts));
-    else e = rows(rows_kernel<D, MX, false>, SmR<D, MX, false>::bytes(mts));
+    if (vt) {
+        using Sm = SmR<D, false, true>;
+        e = allow_smem<rows_kernel<D, false, true>>(Sm::bytes(4));
+        if (e == cudaSuccess) e = launch_pdl(rows_kernel<D, false, true>, grid, block, Sm::bytes(mts), s, tk, tv, r);
+    } else {
+        using Sm = SmR<D, MX, false>;
+        e = allow_smem<rows_kernel<D, MX, false>>(Sm::bytes(4));
+        if (e == cudaSuccess) e = launch_pdl(rows_kernel<D, MX, false>, grid, block, Sm::bytes(mts), s, tk, tv, r);
+    }
     if (e != cudaSuccess) return e;
     MergeParams m = {};
     m.pre_stat = r.pre_stat;
@@ -1988,7 +2062,7 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     m.pre_rows = w.pre_rows;
     m.n_rt = w.n_rt;
     m.unit = few ? kBlk : kKeys;
-    m.lg_at_once = few ? lg_slices(q.n_rows) : kLgMinTiles;
+    m.lg_at_once = few ? lg_slices(q.n_rows) : (w.pre_rows == 128 ? 1 : 0);
     m.T = a.T;
     m.G = q.G;
     m.R = q.R;
