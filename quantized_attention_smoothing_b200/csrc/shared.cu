@@ -8,7 +8,7 @@
 // So every part of every row may be computed anywhere, and the launches are
 //   1. query_kernel: the query rows rotated and quantised;
 //   2. prefix_kernel: the prefix's keys against the B T G rows of each kv head,
-//      128 or 256 rows a CTA (with at most 64 rows, rows_kernel does this);
+//      128 or 256 rows a CTA (with at most 64 rows, rows_kernel does 1 and 2);
 //   3. rows_kernel: each sequence's own keys; it reads nothing of 2, so its
 //      CTAs start as those of 2 leave;
 //   4. shared_merge_kernel.
@@ -266,26 +266,22 @@ struct QueryParams {
     int64_t qs0, qs1, qs2, qs3;
     int q_vec, n_rows, rows_pad, R, G;
     uint8_t* codes;                          // [Hk][rows_pad][D]
-    uint8_t* img;                            // null where no prefix_kernel reads it
+    uint8_t* img;
     float* scale;                            // [Hk][rows_pad]
 };
 
-template <int D, bool MX>
-__global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
-    constexpr int kQe = D / 4, kLgQe = D == 128 ? 5 : 4, kQRow = MX ? 2 * D : D;
-    pdl_launch_dependents();
-    const int n = blockIdx.x * 32 + (threadIdx.x >> 2), qq = threadIdx.x & 3, hk = blockIdx.y;
-    const bool in = n < p.n_rows;
-    const int nn = in ? n : 0, b = nn / p.R, r = nn % p.R;
-    pdl_wait();
-    const uint16_t* src =
-        p.q + b * p.qs0 + (r / p.G) * p.qs1 + (int64_t)(hk * p.G + r % p.G) * p.qs2 + (int64_t)(qq * kQe) * p.qs3;
+// Quarter qq of a query row (src: its first element), held by four neighbouring
+// threads: the row rotated and quantised, this quarter's codes four a word.
+// Returns the row's scale.
+template <int D>
+__device__ __forceinline__ float quantise_quarter(const uint16_t* src, int64_t sd, bool vec, int qq, uint32_t (&w)[D / 16]) {
+    constexpr int kQe = D / 4, kLgQe = D == 128 ? 5 : 4;
     float x[kQe];
-    if (p.q_vec) {
+    if (vec) {
 #pragma unroll
         for (int c = 0; c < kQe / 8; ++c) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + c);
-            const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + c);
+            const uint32_t wd[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 x[8 * c + 2 * e] = __uint_as_float(wd[e] << 16);
@@ -294,7 +290,7 @@ __global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
         }
     } else {
 #pragma unroll
-        for (int d = 0; d < kQe; ++d) x[d] = __uint_as_float(static_cast<uint32_t>(__ldg(src + d * p.qs3)) << 16);
+        for (int d = 0; d < kQe; ++d) x[d] = __uint_as_float(static_cast<uint32_t>(__ldg(src + d * sd)) << 16);
     }
 #pragma unroll
     for (int lg = 0; lg < kLgQe; ++lg) {
@@ -321,38 +317,48 @@ __global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
     for (int d = 0; d < kQe; ++d) amax = fmaxf(amax, fabsf(x[d]));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const float rr = amax != 0.0f ? __fdiv_rn(448.0f, amax) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < D / 16; ++e) {
+        const uint32_t lo16 = e4m3x2_rn_satfinite(__fmul_rn(x[4 * e], rr), __fmul_rn(x[4 * e + 1], rr));
+        const uint32_t hi16 = e4m3x2_rn_satfinite(__fmul_rn(x[4 * e + 2], rr), __fmul_rn(x[4 * e + 3], rr));
+        w[e] = amax != 0.0f ? (lo16 | (hi16 << 16)) : 0u;
+    }
+    return amax != 0.0f ? __fdiv_rn(amax, 448.0f) : 0.0f;
+}
+
+template <int D, bool MX>
+__global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
+    constexpr int kQe = D / 4, kQRow = MX ? 2 * D : D;
+    pdl_launch_dependents();
+    const int n = blockIdx.x * 32 + (threadIdx.x >> 2), qq = threadIdx.x & 3, hk = blockIdx.y;
+    const bool in = n < p.n_rows;
+    const int nn = in ? n : 0, b = nn / p.R, r = nn % p.R;
+    pdl_wait();
+    uint32_t w4[D / 16];
+    const float s = quantise_quarter<D>(p.q + b * p.qs0 + (r / p.G) * p.qs1 + (int64_t)(hk * p.G + r % p.G) * p.qs2 +
+                                            (int64_t)(qq * kQe) * p.qs3, p.qs3, p.q_vec, qq, w4);
     if (!in) return;
-    const float s = amax != 0.0f ? __fdiv_rn(amax, 448.0f) : 0.0f, rr = amax != 0.0f ? __fdiv_rn(448.0f, amax) : 0.0f;
     if (qq == 0) p.scale[(size_t)hk * p.rows_pad + n] = s;
     const int qg = n & 127;                       // row of its 128-row tile
     uint8_t* img = p.img + ((size_t)hk * p.rows_pad + (n & ~127)) * kQRow;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
-        uint32_t w4[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int d = 16 * c + 4 * e;
-            const uint32_t lo16 = e4m3x2_rn_satfinite(__fmul_rn(x[d], rr), __fmul_rn(x[d + 1], rr));
-            const uint32_t hi16 = e4m3x2_rn_satfinite(__fmul_rn(x[d + 2], rr), __fmul_rn(x[d + 3], rr));
-            w4[e] = amax != 0.0f ? (lo16 | (hi16 << 16)) : 0u;
-        }
         const int chunk = (D / 64) * qq + c;
-        *reinterpret_cast<uint4*>(p.codes + ((size_t)hk * p.rows_pad + n) * D + 16 * chunk) =
-            make_uint4(w4[0], w4[1], w4[2], w4[3]);
-        if (p.img == nullptr) continue;
+        const uint4 u = make_uint4(w4[4 * c], w4[4 * c + 1], w4[4 * c + 2], w4[4 * c + 3]);
+        *reinterpret_cast<uint4*>(p.codes + ((size_t)hk * p.rows_pad + n) * D + 16 * chunk) = u;
         if constexpr (MX) {
             // pair m of eight channels = (channel m, channel m + 4)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
                 const int k8 = 2 * chunk + hh;
-                const uint32_t wa = w4[2 * hh], wb = w4[2 * hh + 1];
+                const uint32_t wa = w4[4 * c + 2 * hh], wb = w4[4 * c + 2 * hh + 1];
                 *reinterpret_cast<uint4*>(img + (k8 >> 3) * (128 * 128) + qg * 128 + (((k8 & 7) ^ (qg & 7)) << 4)) =
                     make_uint4(e4m3_pick_to_bf16x2<0>(wa, wb), e4m3_pick_to_bf16x2<1>(wa, wb),
                                e4m3_pick_to_bf16x2<2>(wa, wb), e4m3_pick_to_bf16x2<3>(wa, wb));
             }
         } else {
-            *reinterpret_cast<uint4*>(img + qg * D + (e4m3_chunk<D>(chunk, qg) << 4)) =
-                make_uint4(w4[0], w4[1], w4[2], w4[3]);
+            *reinterpret_cast<uint4*>(img + qg * D + (e4m3_chunk<D>(chunk, qg) << 4)) = u;
         }
     }
 }
@@ -1233,6 +1239,9 @@ __host__ __device__ inline int lg_slices(int rows) { return rows <= 16 ? 2 : (ro
 struct RowsParams {
     const uint8_t* q8;                       // [Hk][rows_pad][D] e4m3 codes
     const float* q_scale;                    // [Hk][rows_pad]
+    const uint16_t* q;                       // or (q8 null) the queries, which every CTA quantises for its rows
+    int64_t qs0, qs1, qs2, qs3;
+    int q_vec;
     const float* ksc;
     const float* vsc;
     const uint8_t* ksf;
@@ -1264,7 +1273,8 @@ struct SmR {
     static constexpr int kScale = kRowsWarps * kStage;
     static constexpr int kStat = kScale + kRowsWarps * 2 * 4 * kBlk;
     static constexpr int kSpan = kStat + kRowsWarps * 16 * 8;        // lowest, highest key any row sees
-    static constexpr int kBar = kSpan + 8;                           // [warp][k | v], then [warp] abort flags
+    static constexpr int kQs = kSpan + 8;                            // [64] query scales
+    static constexpr int kBar = kQs + 64 * 4;                        // [warp][k | v], then [warp] abort flags
     static constexpr int kQf = (kBar + kRowsWarps * 20 + 15) & ~15;  // [m-tile][step][lane] query fragments
     // with m-tiles of 16 rows; three CTAs an SM with one, two with more
     static constexpr int bytes(int mts) { return 1024 + kQf + mts * kSteps * 32 * 16; }
@@ -1346,7 +1356,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
     float cq[2];                                 // base-2 logit = (S k_scale) cq; > 0 keeps a masked -inf
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const bool in = live && r0 + 8 * r < rows;
+        const bool in = p.q8 != nullptr && live && r0 + 8 * r < rows;
         const size_t n = (size_t)hk * p.rows_pad + n0 + r0 + 8 * r;
 #pragma unroll
         for (int k = 0; k < D / 64; ++k)
@@ -1481,7 +1491,34 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
     // mma.sync is made of conversions and fp16 products on this machine, the
     // queries' anew for every key tile); for an MXFP4 cache bf16, pairs
     // (m, m + 4) of eight channels as e2m1_block_to_bf16 orders K's
-    if (live && slice == 0) {
+    float* qs = reinterpret_cast<float*>(sm + Sm::kQs);
+    if (p.q8 == nullptr) {
+        // four threads a row, which write what the other branch writes below
+        const int qq = tid & 3;
+        for (int rr = tid >> 2; (rr & ~7) < 16 * mts; rr += 8 * kRowsWarps) {
+            const int n = rr < rows ? n0 + rr : n0, bb = pre ? fast_div(n, p.div_r) : b, ro = n - bb * p.R;
+            const int t = fast_div(ro, p.div_g);
+            uint32_t w[kSteps];
+            const float x = quantise_quarter<D>(p.q + bb * p.qs0 + t * p.qs1 + (int64_t)(hk * p.G + ro - t * p.G) * p.qs2 +
+                                                    (int64_t)(qq * (D / 4)) * p.qs3, p.qs3, p.q_vec, qq, w);
+            if (qq == 0) qs[rr] = rr < rows ? x : 0.0f;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(qf + ((rr >> 4) * kSteps * 32 + 4 * (rr & 7) + qq)) + ((rr >> 3) & 1);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                uint32_t a, c2;
+                if constexpr (MX) {
+                    const uint32_t wa = w[s & ~1], wb = w[s | 1];
+                    a = (s & 1) ? e4m3_pick_to_bf16x2<2>(wa, wb) : e4m3_pick_to_bf16x2<0>(wa, wb);
+                    c2 = (s & 1) ? e4m3_pick_to_bf16x2<3>(wa, wb) : e4m3_pick_to_bf16x2<1>(wa, wb);
+                } else {
+                    a = e4m3_lo_to_f16x2(w[s]);
+                    c2 = e4m3_hi_to_f16x2(w[s]);
+                }
+                dst[s * 128] = rr < rows ? a : 0u;
+                dst[s * 128 + 2] = rr < rows ? c2 : 0u;
+            }
+        }
+    } else if (live && slice == 0) {
         const uint32_t* w0 = reinterpret_cast<const uint32_t*>(u[0]);
         const uint32_t* w1 = reinterpret_cast<const uint32_t*>(u[1]);
 #pragma unroll
@@ -1502,9 +1539,12 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
             qf[(mt * kSteps + s) * 32 + lane] = a;
         }
     }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) cq[r] = fmaxf(cq[r] * p.logit_scale_log2, FLT_MIN);
     __syncthreads();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        if (p.q8 == nullptr && live) cq[r] = qs[r0 + 8 * r];
+        cq[r] = fmaxf(cq[r] * p.logit_scale_log2, FLT_MIN);
+    }
 
     // key (of the block) of element x of this thread's pair in n-tile j
     auto key_of = [&](int j, int x) { return VT ? 16 * c + 2 * j + x : 8 * j + 2 * c + x; };
@@ -1844,9 +1884,9 @@ SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
     w.own_stat = take(own * sizeof(float2));
     w.pre_o = take(pre * D * sizeof(float));
     w.own_o = take(own * D * sizeof(float));
-    w.codes = take(q_rows * D);
+    w.codes = take(few ? 0 : q_rows * D);
     w.img = take(few ? 0 : q_rows * 2 * D);                  // (bf16 images for an MXFP4 cache)
-    w.q_scale = take(q_rows * sizeof(float));
+    w.q_scale = take(few ? 0 : q_rows * sizeof(float));
     w.bytes = at;
     return w;
 }
@@ -1981,9 +2021,10 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     q.n_rows = a.B * q.R;
     q.rows_pad = w.rows_pad;
     q.codes = ws + w.codes;
-    q.img = few ? nullptr : ws + w.img;
+    q.img = ws + w.img;
     q.scale = reinterpret_cast<float*>(ws + w.q_scale);
-    cudaError_t e = launch_pdl(query_kernel<D, MX>, dim3((unsigned)ceil_div(q.n_rows, 32), a.Hk), dim3(128), 0, s, q);
+    cudaError_t e = cudaSuccess;
+    if (!few) e = launch_pdl(query_kernel<D, MX>, dim3((unsigned)ceil_div(q.n_rows, 32), a.Hk), dim3(128), 0, s, q);
     if (e != cudaSuccess) return e;
     // boxes of half a 128-token page; a transposed V also whole, for prefix_kernel
     CUtensorMap tk, tv, tv128;
@@ -2002,8 +2043,14 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     RowsParams r = {};
-    r.q8 = q.codes;
+    r.q8 = few ? nullptr : q.codes;
     r.q_scale = q.scale;
+    r.q = q.q;
+    r.qs0 = q.qs0;
+    r.qs1 = q.qs1;
+    r.qs2 = q.qs2;
+    r.qs3 = q.qs3;
+    r.q_vec = q.q_vec;
     r.ksc = a.k_scale;
     r.vsc = a.v_scale;
     r.ksf = a.k_sf;
