@@ -25,6 +25,7 @@
 // ctx_b - (offset_{b+1} - t).
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "sage_internal.h"
 #include "sage_ptx.cuh"
@@ -39,7 +40,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kRowsPer = kPlanMaxRows / kThreads;      // lengths a thread sums at most
 // slots the cluster writes itself: 8 CTAs x 1024 threads x 4 slots, twice
 constexpr int kInlineTokens = 65536;
-constexpr int kSlotThreads = 256, kSlotPer = 8192;     // slot kernel: slots per CTA
+constexpr int kSlotThreads = 256, kSlotPer = 2048;     // slot kernel: slots per CTA
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -58,17 +59,23 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// The row whose range [off[b], off[b + 1]) holds i (off[0] = 0 <= i < off[n]):
-// the last b with off[b] <= i.
-__device__ __forceinline__ int find_row(const int* off, int n, int i) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (off[mid] <= i) lo = mid;
-        else hi = mid - 1;
+// For U numbers at once, the row whose range [off[b], off[b + 1]) holds i
+// (off[0] = 0 <= i < off[n]): the last b with off[b] <= i. step: the largest
+// power of two below n (0 for n = 1).
+template <int U>
+__device__ __forceinline__ void find_rows(const int* off, int n, int step, const int* i, int* b) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) b[u] = 0;
+    for (; step > 0; step >>= 1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int x = b[u] + step;
+            if (x < n && off[x] <= i[u]) b[u] = x;
+        }
     }
-    return lo;
 }
+
+__device__ __forceinline__ int first_step(int n) { return n > 1 ? 1 << (31 - __clz(n - 1)) : 0; }
 
 struct Sum3 {
     long long tok, need, gone;
@@ -191,21 +198,59 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const PlanParams p) {
         const int s = start_of[b];
         return s < 0 ? ~s : s;
     };
-    // the i-th page given back, the k-th page handed out
-    auto gone_page = [&](int i) {
-        const int b = find_row(gone_off, p.B, i);
-        return p.table[(int64_t)b * p.max_pages + p.prefix_pages + i - gone_off[b]];
+    // U things a thread at a time, searches and loads of all of them before
+    // any store: with many things the loops are bound by their chains of
+    // dependent accesses (62000 new entries: 17.9 us one by one, 11.7 with four
+    // at a time), with few by the searches themselves, dummies' included
+    const int step = first_step(p.B);
+    // the i-th pages given back
+    auto gone_pages = [&](auto u_c, const int* i, const bool* in, int* pg) {
+        constexpr int U = decltype(u_c)::value;
+        int b[U];
+        find_rows<U>(gone_off, p.B, step, i, b);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (in[u]) pg[u] = p.table[(int64_t)b[u] * p.max_pages + p.prefix_pages + i[u] - gone_off[b[u]]];
     };
-    auto new_page = [&](int k) {
-        const int at = top - 1 - k;
-        return at < fc ? p.free_list[at] : gone_page(at - fc);
+    // the k-th pages handed out
+    auto new_pages = [&](auto u_c, const int* k, const bool* in, int* pg) {
+        constexpr int U = decltype(u_c)::value;
+        int g[U];
+        bool back[U], any = false;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int at = top - 1 - k[u];
+            back[u] = in[u] && at >= fc;
+            g[u] = max(0, at - fc);
+            any |= back[u];
+            if (in[u] && at < fc) pg[u] = p.free_list[at];
+        }
+        if (any) gone_pages(u_c, g, back, pg);
+    };
+    // body(u_c, first, stride) for the things first, first + stride, .. of n
+    auto batches = [&](int n, auto body) {
+        int i = gtid;
+        for (; i + 3 * (int64_t)nthr < n; i += 4 * nthr) body(std::integral_constant<int, 4>{}, i);
+        for (; i < n; i += nthr) body(std::integral_constant<int, 1>{}, i);
     };
     // ---- new table entries
-    for (int k = gtid; k < na; k += nthr) {
-        const int b = find_row(need_off, p.B, k);
-        const int held = (start_at(b) + page - 1) >> lg;
-        p.table[(int64_t)b * p.max_pages + held + k - need_off[b]] = new_page(k);
-    }
+    batches(na, [&](auto u_c, int k0) {
+        constexpr int U = decltype(u_c)::value;
+        int k[U], b[U], pg[U];
+        bool in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            in[u] = true;
+            k[u] = k0 + u * nthr;
+        }
+        find_rows<U>(need_off, p.B, step, k, b);
+        new_pages(u_c, k, in, pg);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int held = (start_at(b[u]) + page - 1) >> lg;
+            p.table[(int64_t)b[u] * p.max_pages + held + k[u] - need_off[b[u]]] = pg[u];
+        }
+    });
     // ---- the prefix's entries for the requests that join
     if (p.prefix_pages > 0) {
         for (int b = gtid >> 5; b < p.B; b += nthr >> 5)
@@ -214,20 +259,43 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const PlanParams p) {
                     p.table[(int64_t)b * p.max_pages + e] = p.prefix[e];
     }
     // ---- pages given back and not handed out again stay on the list
-    for (int i = gtid; i < nf - na; i += nthr) p.free_list[fc + i] = gone_page(i);
+    batches(nf - na, [&](auto u_c, int i0) {
+        constexpr int U = decltype(u_c)::value;
+        int i[U], pg[U];
+        bool in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            in[u] = true;
+            i[u] = i0 + u * nthr;
+        }
+        gone_pages(u_c, i, in, pg);
+#pragma unroll
+        for (int u = 0; u < U; ++u) p.free_list[fc + i[u]] = pg[u];
+    });
     // ---- slots
     if (p.inline_slots) {
-        for (int t = gtid; t < p.max_tokens; t += nthr) {
-            int slot = -1;
-            if (t < tok_off[p.B]) {
-                const int b = find_row(tok_off, p.B, t);
-                const int start = start_at(b), pos = start + t - tok_off[b], e = pos >> lg;
-                const int held = (start + page - 1) >> lg;
-                const int pg = e < held ? p.table[(int64_t)b * p.max_pages + e] : new_page(need_off[b] + e - held);
-                slot = (pg << lg) + (pos & (page - 1));
+        batches((int)n_tok, [&](auto u_c, int t0) {
+            constexpr int U = decltype(u_c)::value;
+            int t[U], b[U], k[U], pg[U], pos[U];
+            bool fresh[U], any = false;
+#pragma unroll
+            for (int u = 0; u < U; ++u) t[u] = t0 + u * nthr;
+            find_rows<U>(tok_off, p.B, step, t, b);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int start = start_at(b[u]), held = (start + page - 1) >> lg;
+                pos[u] = start + t[u] - tok_off[b[u]];
+                const int e = pos[u] >> lg;
+                fresh[u] = e >= held;
+                k[u] = fresh[u] ? need_off[b[u]] + e - held : 0;
+                any |= fresh[u];
+                if (!fresh[u]) pg[u] = p.table[(int64_t)b[u] * p.max_pages + e];
             }
-            p.slots[t] = slot;
-        }
+            if (any) new_pages(u_c, k, fresh, pg);
+#pragma unroll
+            for (int u = 0; u < U; ++u) p.slots[t[u]] = (pg[u] << lg) + (pos[u] & (page - 1));
+        });
+        for (int t = (int)n_tok + gtid; t < p.max_tokens; t += nthr) p.slots[t] = -1;
     }
     cluster_wait();                          // every CTA has read the lengths
     for (int b = gtid; b < p.B; b += nthr) {
@@ -254,34 +322,46 @@ __global__ void __launch_bounds__(kSlotThreads) slot_kernel(const int32_t* __res
     pdl_launch_dependents();
     for (int b = threadIdx.x; b <= B; b += kSlotThreads) off[b] = __ldg(offsets + b);
     __syncthreads();
-    const int n_tok = off[B];
-    const int64_t end = min((int64_t)max_tokens, ((int64_t)blockIdx.x + 1) * kSlotPer);
-#pragma unroll 2
-    for (int64_t t0 = (int64_t)blockIdx.x * kSlotPer + 4 * threadIdx.x; t0 < end; t0 += 4 * kSlotThreads) {
+    const int n_tok = off[B], step = first_step(B);
+    constexpr int U = kSlotPer / (4 * kSlotThreads);     // runs of four slots a thread
+    int t[U], b[U], last[U];                             // position of token x: last + x
+    const int64_t t00 = (int64_t)blockIdx.x * kSlotPer + 4 * threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < U; ++u) t[u] = (int)min(t00 + u * 4 * kSlotThreads, (int64_t)max(n_tok - 1, 0));
+    find_rows<U>(off, B, step, t, b);
+#pragma unroll
+    for (int u = 0; u < U; ++u) last[u] = __ldg(ctx + b[u]) - off[b[u] + 1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t t0 = t00 + u * 4 * kSlotThreads;
         int s[4] = {-1, -1, -1, -1};
         if (t0 < n_tok) {
-            int b = find_row(off, B, (int)t0);
-            int last = __ldg(ctx + b) - off[b + 1];      // position of token t: last + t
+            int e = -1, pg = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = (int)t0 + i;
-                if (t < n_tok) {
-                    if (t >= off[b + 1]) {
-                        do ++b;
-                        while (t >= off[b + 1]);
-                        last = __ldg(ctx + b) - off[b + 1];
+                const int x = (int)t0 + i;
+                if (x < n_tok) {
+                    if (x >= off[b[u] + 1]) {
+                        do ++b[u];
+                        while (x >= off[b[u] + 1]);
+                        last[u] = __ldg(ctx + b[u]) - off[b[u] + 1];
+                        e = -1;
                     }
-                    const int pos = last + t;
-                    s[i] = (__ldg(table + (int64_t)b * max_pages + (pos >> lg)) << lg) + (pos & ((1 << lg) - 1));
+                    const int pos = last[u] + x;
+                    if ((pos >> lg) != e) {
+                        e = pos >> lg;
+                        pg = __ldg(table + (int64_t)b[u] * max_pages + e);
+                    }
+                    s[i] = (pg << lg) + (pos & ((1 << lg) - 1));
                 }
             }
         }
-        if (vec && t0 + 4 <= end) {
+        if (vec && t0 + 4 <= max_tokens) {
             *reinterpret_cast<int4*>(slots + t0) = make_int4(s[0], s[1], s[2], s[3]);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (t0 + i < end) slots[t0 + i] = s[i];
+                if (t0 + i < max_tokens) slots[t0 + i] = s[i];
         }
     }
 }
