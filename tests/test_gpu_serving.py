@@ -471,6 +471,118 @@ def test_shared_reports_bad_pages_and_lengths(handles):
     assert sage.sage_device_error() == sage.SAGE_OK
 
 
+@pytest.mark.parametrize("seed", range(32))
+def test_shared_random_shapes(handles, seed):
+    """Sizes drawn over what the interface takes: row counts on both sides of
+    64, 128 and 256, every page size, 1 to 64 rows a sequence, prefixes that end
+    anywhere, windows, rows that see nothing."""
+    rng = np.random.default_rng(1000 + seed)
+    fmt = ["token", "tensor", "mxfp4", "token_vt", "tensor_vt"][seed % 5]
+    D = 128 if fmt == "mxfp4" or seed % 3 else 64
+    page = 128 if fmt.endswith("vt") else int(rng.choice([16, 32, 64, 128]))
+    G, T, Hk = int(rng.integers(1, 17)), int(rng.integers(1, 5)), int(rng.integers(1, 4))
+    B = int(max(1, min(40, rng.choice([60, 120, 250, 500]) // (G * T))))
+    prefix = int(rng.choice([0, 1, rng.integers(1, 900), rng.integers(1, 2000)]))
+    most = max(2, min(600, 30000 // (B * T)))
+    ctx = [int(prefix + rng.integers(0, most)) if rng.random() < 0.85 else int(rng.integers(0, prefix + 1)) for _ in range(B)]
+    window = int(rng.choice([10 ** 6, 2 ** 31 - 1, rng.integers(1, prefix + most + 1)]))
+    d = sh.make_shared(B, T, G * Hk, Hk, D, page, prefix, ctx, seed=seed, fmt=fmt)
+    out = run_shared(handles[D], d, page, window, 1.0 / math.sqrt(D))
+    torch.cuda.synchronize()
+    assert sage.sage_device_error() == sage.SAGE_OK
+    check_shared(out, d, window, 1.0 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("B,prefix,ctx", [(5, 700, [702, 900, 760, 1300, 701]), (1, 300, [900])])
+def test_shared_value_scales_far_apart(handles, B, prefix, ctx):
+    """Value scales that differ by 2^12 inside a tile, and whole runs of keys
+    2^10 larger than those before them (the exponent they are held against
+    moves). fp16 keeps 2^-25 of the largest scale, 2^-13 of the smallest one's
+    unit, so the bf16-step tolerance holds as it is."""
+    d = sh.make_shared(B, 2, 16, 1, 128, 64, prefix, ctx, seed=31)
+    g = torch.Generator().manual_seed(6)
+    f = torch.exp2(torch.randint(-6, 7, d["vs"].shape, generator=g).float())
+    order = {int(pg): i for i, pg in enumerate(d["prefix"].tolist())}
+    for pg in range(d["pages"]):
+        f[pg] *= 2.0 ** (5 if order.get(pg, pg) % 7 > 3 else -5)
+    d["vs"] = d["vs"] * f
+    out = run_shared(handles[128], d, 64, 9999, 0.09)
+    check_shared(out, d, 9999, 0.09)
+
+
+def test_shared_and_append_far_into_a_large_cache(handles):
+    """Caches of over 2^32 bytes: pages at their far end give the same bits as
+    the same pages in a small cache, for reading and for writing."""
+    Hk, D, page, pages = 8, 128, 128, 36000
+    for B, T in ((2, 1), (9, 2)):
+        d = sh.make_shared(B, T, 32, Hk, D, page, 300, [300 + 40 * (i + 1) for i in range(B)], seed=B)
+        small = run_shared(handles[D], d, page, 9999, 0.09)
+        far = {n: torch.zeros((pages,) + tuple(d[n].shape[1:]), dtype=d[n].dtype, device="cuda")
+               for n in ("kc", "vc", "ks", "vs")}
+        n = d["pages"]
+        for k in far:
+            far[k][pages - n:] = d[k].cuda().flip(0)
+        big = dict(d, pages=pages, prefix=pages - 1 - d["prefix"],
+                   table=torch.where(d["table"] > 1 << 20, d["table"], pages - 1 - d["table"]))
+        out = torch.empty_like(small)
+        sage.sage_attn_decode_shared(handles[D], big["q"].cuda(), far["kc"], far["vc"], far["ks"], far["vs"],
+                                     big["prefix"].cuda(), big["length"].cuda(), big["table"].cuda(), big["ctx"].cuda(),
+                                     page, pages, 9999, 0.09, out)
+        assert sage.sage_device_error() == sage.SAGE_OK
+        assert torch.equal(out, small)
+    k, v, slots, mean, few = append_inputs(200, Hk, D, page, 5)
+    near = [torch.zeros((few, Hk, page, D), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    near_s = [torch.zeros((few, Hk, page), device="cuda") for _ in range(2)]
+    sage.sage_kv_append(handles[D], k, v, slots.cuda(), *near, *near_s, k_mean=mean.cuda())
+    for t in far.values():
+        t[pages - few:] = 0
+    moved = torch.where(slots >= 0, slots + (pages - few) * page, slots).int()
+    sage.sage_kv_append(handles[D], k, v, moved.cuda(), far["kc"], far["vc"], far["ks"], far["vs"], k_mean=mean.cuda())
+    assert sage.sage_device_error() == sage.SAGE_OK
+    for a, b in zip(near + near_s, (far["kc"], far["vc"], far["ks"], far["vs"])):
+        assert torch.equal(a, b[pages - few:])
+
+
+@pytest.mark.parametrize("B,T", [(2, 1), (20, 2)])
+def test_shared_two_at_once(handles, B, T):
+    """Two calls on two streams at once, each with its workspace, and two
+    captured graphs replayed at once: the results of one after the other. A
+    call's result does not depend on the run."""
+    ds = [sh.make_shared(B, T, 16, 1, 128, 64, 1500, [1500 + 30 * (i + 1) for i in range(B)], seed=s) for s in (1, 2)]
+    h = handles[128]
+    want = [run_shared(h, d, 64, 9999, 0.09) for d in ds]
+    gpu = [{n: d[n].cuda() for n in ("q", "kc", "vc", "ks", "vs", "prefix", "length", "table", "ctx")} for d in ds]
+    ws = [torch.empty((sage.sage_attn_decode_shared_workspace(B, T, 16, 1, 128),), dtype=torch.uint8, device="cuda")
+          for _ in ds]
+    outs = [torch.zeros_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in ds]
+
+    def call(i):
+        t = gpu[i]
+        sage.sage_attn_decode_shared(h, t["q"], t["kc"], t["vc"], t["ks"], t["vs"], t["prefix"], t["length"], t["table"],
+                                     t["ctx"], 64, ds[i]["pages"], 9999, 0.09, outs[i], ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i in range(2):
+            call(i)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    graphs = [torch.cuda.CUDAGraph() for _ in ds]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            for _ in range(10):
+                call(i)
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    for i in range(2):
+        with torch.cuda.stream(streams[i]):
+            graphs[i].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    assert sage.sage_device_error() == sage.SAGE_OK
+
+
 # ------------------------------------------------------------- all together
 
 @pytest.mark.parametrize("fmt,page,Hk,side", [("token", 32, 2, False), ("tensor_vt", 128, 1, True),
