@@ -10,13 +10,16 @@
 //   2. prefix_kernel: the prefix's keys against the B T G rows of each kv head,
 //      128 or 256 rows a CTA (with at most 64 rows, rows_kernel does 1 and 2);
 //   3. rows_kernel: each sequence's own keys; it reads nothing of 2, so its
-//      CTAs start as those of 2 leave;
+//      CTAs run on the SMs that 2 leaves over and start as those of 2 leave;
 //   4. shared_merge_kernel.
 // What bounds 2: reading K and V once is cheap (the point of the operator);
-// for rows R and keys L the SMs do 2 R L D FP8 + 2 R L D bf16 MACs and R L
-// exponentials. At 128 rows x 128 keys that is 256 + 512 tensor cycles and
-// 1024 MUFU cycles an SM, so the exponential bounds a full tile and the two
-// row groups of a CTA keep it busy in turn.
+// for rows R and keys L the SMs do 2 R L D FP8 + 2 R L D fp16 FLOPs and R L
+// exponentials: 31 us of tensor time and 30 us of MUFU for 4096 rows, 32768
+// keys and D 128, where the kernel takes 74. No pipe is full (MUFU 39 %,
+// tensor 33 %, issue 44 %): a unit of 128 rows x 64 keys is a chain of 2250
+// cycles in two softmax warps a scheduler, and what was tried against that
+// (four warps a scheduler, turns, earlier loads of S, fewer exponentials on
+// MUFU, naps instead of polls, PV without its wait) gained nothing or lost.
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -256,9 +259,10 @@ __global__ void __launch_bounds__(32 * W) shared_merge_kernel(const MergeParams 
 // The query rows of every sequence, once for all CTAs: row n = (b T + t) G + g
 // of kv head hk rotated (fp32 butterfly) and quantised to e4m3 with scale
 // max|q_hat| / 448 (the operations of decode.cu). The codes go out row by row
-// for rows_kernel, and for prefix_kernel as images of its shared-memory operand: per 128-row tile [128][D] codes in
-// the swizzle of a D-byte row, or (MXFP4 cache) the codes' exact bf16 values,
-// two 64-channel atoms [128][128 B], channels in the converters' order for K.
+// for rows_kernel, and for prefix_kernel as images of its shared-memory
+// operand: per 128-row tile [128][D] codes in the swizzle of a D-byte row, or
+// (MXFP4 cache) the codes' exact bf16 values, two 64-channel atoms [128][128 B],
+// channels in the converters' order for K.
 // (In the prefix CTAs themselves this took 14500 cycles, 4 passes of 64 rows,
 // repeated by every split.) Four threads a row.
 struct QueryParams {
@@ -367,7 +371,8 @@ __global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
 //   warps 0-7   softmax, two groups of four; thread = one query row (TMEM lane)
 //               and all 128 keys of a unit, so the row statistics need no
 //               shuffles;
-//   warps 8-11  V converters: e4m3 -> exact fp16 (MXFP4: K and V -> bf16);
+//   warps 8-11  V converters: e4m3 -> fp16, the value's scale multiplied in
+//               (MXFP4: K and V -> bf16, exactly);
 //   warp 12     K/V producer (one TMA box per page), warps 13 and 15 MMA
 //               issuers of groups 0 and 1, warp 14 scale producer.
 // A unit is one 128-row x 64-key block of S: half h of a key tile, for group g.
@@ -376,14 +381,16 @@ __global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
 // and converted once for 256 rows. RG = 1 (128 rows): both groups hold the
 // same rows, group g takes the tiles of parity g, the units of tile i are
 // w = 2 i + h, and the groups' (m, l, O) are combined at the end.
-// Per unit: S = Q8 K8^T (TMEM, fp32, M = 128, N = 64) -> y = S k_scale -> row
-// max -> p = 2^(y c - m) -> P = fp16(p v_scale 2^-e) (MXFP4: bf16(p)), over S's own columns
-// as the A operand (in TMEM) of O += P V. S buffer [g][h] is used by every
-// fourth unit, so a group computes on one half while the products of the
-// other run: PV(w), then QK(w + 3) once PV(w - 1), which read P from that
-// buffer, has completed. (One 128-key unit a group in flight, its softmax
-// waiting for both products: 1800 of 5500 cycles a unit spent waiting, and 128
-// logits a thread spilled; 120 us against 62 us for 4096 rows x 32768 keys.)
+// Per unit: S = Q8 K8^T (TMEM, fp32, M = 128, N = 64) -> y = S k_scale ->
+// p = 2^(y c - m) -> P = fp16(p) (MXFP4: bf16(p)), over S's own columns as the
+// A operand (in TMEM) of O += P V. S buffer [g][h] is used by every fourth
+// unit, so a group computes on one half while the products of the other run:
+// PV(w), then QK(w + 3) once PV(w - 1), which read P from that buffer, has
+// completed. (One 128-key unit a group in flight, its softmax waiting for both
+// products: 1800 of 5500 cycles a unit spent waiting, and 128 logits a thread
+// spilled. The value scales multiplied into P instead of V, and the unit's
+// maximum taken instead of its sum checked: 100.2 us against 97.2 for a call
+// of 4096 rows and 32768 keys.)
 constexpr int kScStages = 8;                 // scale ring
 constexpr int kThreads = 512;
 constexpr int kConvWarp0 = 8, kTmaWarp = 12, kMmaWarp0 = 13, kScaleWarp = 14, kMmaWarp1 = 15;
@@ -831,14 +838,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t ts = trow + 64 * (2 * g + h);
             ok = warp_all(mbar_wait(&bars[Sm::kSFull + 2 * g + h], (k >> 1) & 1, abort_flag, &g_shared_err, 8));
             if (!ok) break;
-            uint32_t x0[32], x1[32];
             if (h == 0) ok = warp_all(mbar_wait(&bars[Sm::kScFull + c], (i / kScStages) & 1, abort_flag, &g_shared_err, 9));
-            if (!idle) {                                     // (on its way during what comes up to the wait below)
+            if (!ok) break;
+            if (!idle) {
+                // (behind the wait for the scales: before it, or before the last
+                // unit's sum is checked, the loads measured 4 to 7 % slower)
+                uint32_t x0[32], x1[32];
                 tc_fence_after();
                 tmem_ld32(ts, x0);
                 tmem_ld32(ts + 32, x1);
-            }
-            if (!idle) {
                 const int key0 = (tb + i) * kKeys + 64 * h;
                 const int badm = meta[c];
                 const float4* ks = reinterpret_cast<const float4*>(scl + c * Sm::kScSlot + 64 * h);
@@ -882,7 +890,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bool slow = ve != vexp || badm != 0 || key0 + 63 >= L || !__all_sync(0xffffffffu, none || all);
                 tmem_wait_ld(x0);
                 tmem_wait_ld(x1);
-                if (!ok) break;
                 auto fast = [&](auto plain) {
                     const uint64_t nsub2 = f2_pack(-m_run, -m_run);
                     uint64_t lu[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
