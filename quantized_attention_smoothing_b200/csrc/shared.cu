@@ -142,19 +142,20 @@ struct MergeParams {
     const int32_t* ctx;
     int cap_prefix, cap_rows, window, np, ns, pre_rows, n_rt;
     int unit, lg_at_once;                    // keys of a tile or block of the prefix part, used_splits' third
-    int lg_own;                              // a sequence's own: used_splits' third
+    int lg_unit, lg_own;                     // a sequence's own: log2 of its unit, used_splits' third
     int n_rows, R, T, G, Hk;
     __nv_bfloat16* out;
     int64_t os0, os1, os2, os3;
 };
 
-// Blocks [first, first + n) of a sequence's own keys, those of [L, ctx) that
-// one of its T query tokens sees, and the lowest and highest such key.
-__device__ __forceinline__ void own_keys(int ctx, int L, int T, int window, int& lo, int& hi, int& first, int& n) {
+// Blocks [first, first + n) (of 2^lg keys) of a sequence's own keys, those of
+// [L, ctx) that one of its T query tokens sees, and the lowest and highest such
+// key.
+__device__ __forceinline__ void own_keys(int ctx, int L, int T, int window, int lg, int& lo, int& hi, int& first, int& n) {
     lo = max(L, ctx - T - window + 1);
     hi = lo < ctx ? ctx - 1 : -1;
-    first = hi >= 0 ? lo / kBlk : 0;
-    n = hi >= 0 ? hi / kBlk + 1 - first : 0;
+    first = hi >= 0 ? lo >> lg : 0;
+    n = hi >= 0 ? (hi >> lg) + 1 - first : 0;
 }
 
 // CTA: 32 rows (lane = row) x kCh channels; its W warps share out the parts
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(32 * W) shared_merge_kernel(const MergeParams 
     const int L = max(0, min(__ldg(p.plen), p.cap_prefix));
     const int np = L > 0 ? used_splits((L + p.unit - 1) / p.unit, p.np, p.lg_at_once) : 0;
     int lo, hi, first, n_own;
-    own_keys(ctx, L, p.T, p.window, lo, hi, first, n_own);
+    own_keys(ctx, L, p.T, p.window, p.lg_unit, lo, hi, first, n_own);
     const int parts = np + (n_own > 0 ? used_splits(n_own, p.ns, p.lg_own) : 0);
     const int most = __reduce_max_sync(0xffffffffu, parts);
     const size_t part_p = ((size_t)hk * p.n_rt + rt) * p.np, part_o = ((size_t)b * p.Hk + hk) * p.ns;
@@ -407,7 +408,8 @@ constexpr int kPolyEvery = 4;
 
 struct PrefixParams {
     const uint8_t* q_img;                    // [Hk n_rt][RG] 128-row operand tiles, from query_kernel
-    const float* q_scale;                    // [Hk n_rt][128 RG]
+    const uint8_t* codes;                    // OWN: [Hk][rows_pad][D]
+    const float* q_scale;                    // [Hk][rows_pad]
     const float* ksc;
     const float* vsc;
     int per_tensor, v_trans;
@@ -417,10 +419,10 @@ struct PrefixParams {
     const int32_t* plen;
     const int32_t* ctx;
     FastDiv div_r, div_g;
-    int T, Hk, R, n_rows, page, lg_page, cap_prefix, cap_rows, num_pages, window, np, n_rt;
+    int T, Hk, R, n_rows, rows_pad, page, lg_page, max_pages, cap_prefix, cap_rows, num_pages, window, np, n_rt;
     float logit_scale_log2;
-    float2* stat;                            // [Hk n_rt][np][128 RG]
-    float* o;                                // [Hk n_rt][np][D / 4][128 RG][4]
+    float2* stat;                            // [Hk n_rt][np][128 RG]; OWN: [B Hk][np][64]
+    float* o;                                // [Hk n_rt][np][D / 4][128 RG][4]; OWN: [B Hk][np][D / 4][64][4]
 };
 
 template <int D, bool MX, int RG>
@@ -504,7 +506,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-template <int D, bool MX, int RG>
+// OWN (RG = 1): a sequence's own keys instead, its rows (more than 32 of them)
+// in the lower half of the tile, on a grid [B Hk][splits]; launched behind the
+// prefix's kernel, of which it reads nothing.
+template <int D, bool MX, int RG, bool OWN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const PrefixParams p) {
@@ -520,8 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* meta = reinterpret_cast<int*>(sm + Sm::kMeta);
     int* span = reinterpret_cast<int*>(sm + Sm::kSpan);
     float* scl = reinterpret_cast<float*>(sm + Sm::kScale);
-    const int split = blockIdx.x, hk = blockIdx.y / p.n_rt, rt = blockIdx.y % p.n_rt;
-    const int row0 = rt * kRowsCta;
+    const int split = blockIdx.x, seq = OWN ? blockIdx.y / p.Hk : 0;
+    const int hk = OWN ? blockIdx.y - seq * p.Hk : blockIdx.y / p.n_rt;
+    const int row0 = OWN ? seq * p.R : blockIdx.y % p.n_rt * kRowsCta, row_end = OWN ? row0 + p.R : p.n_rows;
+    constexpr int kRowsOut = OWN ? 64 : kRowsCta;    // of a partial
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (warp == kMmaWarp1) {
@@ -548,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    pdl_wait();
+    if (!OWN) pdl_wait();
     pdl_launch_dependents();
 
     // what the set-up reads, requested together: the length, and the softmax
@@ -557,24 +564,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = (warp >> 2) & 1;
     const int r = RG == 2 ? (tid & 255) : (tid & 127);
     const int n = row0 + r;
-    const bool rv = n < p.n_rows;
+    const bool rv = n < row_end;
     int ctx = 0;
     float q_scale = 0.0f;
     if (warp < 8 && rv) {
         ctx = __ldg(p.ctx + fast_div(n, p.div_r));
-        q_scale = __ldcg(p.q_scale + (size_t)blockIdx.y * kRowsCta + r);
+        q_scale = __ldcg(p.q_scale + (size_t)hk * p.rows_pad + n);
     }
     const float ks_t = !MX && p.per_tensor ? __ldg(p.ksc) : 1.0f, vs_t = !MX && p.per_tensor ? __ldg(p.vsc) : 1.0f;
     if (L > p.cap_prefix || L < 0) {
         if (tid == 0 && split == 0) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
         L = max(0, min(L, p.cap_prefix));
     }
-    // the keys of the prefix that the row sees
+    if constexpr (OWN) {
+        if (tid == 0 && split == 0 && (ctx < 0 || ctx > p.cap_rows)) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
+        // the query operand, from the codes (a tile's image has its rows elsewhere)
+        for (int idx = tid; idx < p.R * (D / 16); idx += kThreads) {
+            const int row = idx / (D / 16), ch = idx % (D / 16);
+            const uint4 u = __ldcg(reinterpret_cast<const uint4*>(p.codes + ((size_t)hk * p.rows_pad + row0 + row) * D) + ch);
+            if constexpr (MX) {
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const int k8 = 2 * ch + hh;
+                    const uint32_t wa = hh ? u.z : u.x, wb = hh ? u.w : u.y;
+                    *reinterpret_cast<uint4*>(sm + Sm::kQ + (k8 >> 3) * (128 * 128) + row * 128 + (((k8 & 7) ^ (row & 7)) << 4)) =
+                        make_uint4(e4m3_pick_to_bf16x2<0>(wa, wb), e4m3_pick_to_bf16x2<1>(wa, wb),
+                                   e4m3_pick_to_bf16x2<2>(wa, wb), e4m3_pick_to_bf16x2<3>(wa, wb));
+                }
+            } else {
+                *reinterpret_cast<uint4*>(sm + Sm::kQ + row * D + (e4m3_chunk<D>(ch, row) << 4)) = u;
+            }
+        }
+        fence_proxy_async_smem();
+    }
+    // the keys of the part that the row sees
     int key_lo = INT32_MAX, key_hi = -1;
     if (warp < 8 && rv) {
         const int pq = max(0, min(ctx, p.cap_rows)) - p.T + fast_div(n - fast_div(n, p.div_r) * p.R, p.div_g);
-        key_lo = max(0, pq - p.window + 1);
-        key_hi = min(pq, L - 1);
+        key_lo = max(OWN ? L : 0, pq - p.window + 1);
+        key_hi = OWN ? pq : min(pq, L - 1);
         if (key_hi < key_lo) {
             key_lo = INT32_MAX;
             key_hi = -1;
@@ -604,6 +632,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     share_out(n_all, used_splits(n_all, p.np, RG == 1 ? 1 : 0), split, tb, te);
     const int nt = te - tb;
     tb += t0;
+    // keys that are there: the prefix's, or those that a row sees (a sequence's
+    // pages may hold anything below L)
+    const int there = OWN ? lo : 0, gone = OWN ? hi + 1 : L;
+    const int32_t* ptab = p.ptab + (OWN ? (int64_t)seq * p.max_pages : 0);
     const int ppt = kKeys / p.page;
     const size_t part = (size_t)blockIdx.y * p.np + split;
 
@@ -612,11 +644,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (warp == kTmaWarp || warp == kScaleWarp) {
         // ------------------------------------------------------------ producers
         // (as decode.cu's: lane j of chunk c looks up page 32 c + j of the
-        // CTA's pages; a page that holds no key below L is not looked up)
+        // CTA's pages; a page that holds no key of the part is not looked up)
         const bool kv = warp == kTmaWarp;
         int chunk = -1, phys = 0, issued = 0, vexp = kNoExp;
         bool bad = false, found = false;
-        if (kv && lane == 0 && nt > 0) {
+        if (OWN && kv && lane == 0 && nt > 0) mbar_arrive(&bars[Sm::kQReady]);
+        if (!OWN && kv && lane == 0 && nt > 0) {
             mbar_arrive_expect_tx(&bars[Sm::kQReady], kRowsCta * Sm::kQRow);
             bulk_load(sm + Sm::kQ, p.q_img + (size_t)blockIdx.y * kRowsCta * Sm::kQRow, kRowsCta * Sm::kQRow,
                       &bars[Sm::kQReady]);
@@ -633,8 +666,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int lp = tb * ppt + 32 * chunk + lane;
                 phys = 0;
                 bad = found = false;
-                if (lp < (tb + nt) * ppt && lp * p.page < L) {
-                    const int pg = __ldg(p.ptab + lp);
+                if (lp < (tb + nt) * ppt && lp * p.page < gone && (!OWN || (lp + 1) * p.page > there)) {
+                    const int pg = __ldg(ptab + lp);
                     if (pg < 0 || pg >= p.num_pages) {
                         bad = true;
                         if (kv) atomicCAS(&g_shared_err, 0u, kErrRangeCode);
@@ -651,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(&bars[Sm::kKvFull + s], 2 * (Sm::kKStage + Sm::kSfStage));
                 __syncwarp();
                 if (mine) {
-                    // FP8: a page without a key below L, or off the cache, is read
+                    // FP8: a page without a key of the part, or off the cache, is read
                     // as zeros (a coordinate off the map): what its stand-in holds
                     // could be NaN codes, which a weight of zero does not cancel
                     const int z = MX || found ? phys * p.Hk + hk : -1, q = lane - slot0;
@@ -679,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bars[Sm::kScFull + c]);
                 } else {
                     // keys 4 lane .. 4 lane + 3: k_scale, and v_scale relative to
-                    // 2^vexp, zero where the slot holds no key of the prefix
+                    // 2^vexp, zero where the slot holds no key of the part
                     float ks[4], vs[4];
                     const int pq = __shfl_sync(0xffffffffu, phys, slot0 + 4 * lane / p.page);
                     const int64_t src = ((int64_t)pq * p.Hk + hk) * p.page + (4 * lane) % p.page;
@@ -887,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int ve = MX ? 0 : meta[kScStages + c];
                 if (vexp == kNoExp) vexp = ve;               // (no key before: O holds zeros)
                 const bool none = key_hi < key0 || key_lo > key0 + 63, all = key_lo <= key0 && key_hi >= key0 + 63;
-                bool slow = ve != vexp || badm != 0 || key0 + 63 >= L || !__all_sync(0xffffffffu, none || all);
+                bool slow = ve != vexp || badm != 0 || key0 + 63 >= gone || (OWN && key0 < there) || !__all_sync(0xffffffffu, none || all);
                 tmem_wait_ld(x0);
                 tmem_wait_ld(x1);
                 auto fast = [&](auto plain) {
@@ -1012,13 +1045,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         // four channels, of columns j .. of O (MX: the eight columns of a group
         // hold channels 0 4 1 5 2 6 3 7)
-        float4* po = reinterpret_cast<float4*>(p.o) + part * (D / 4) * kRowsCta + r;
+        float4* po = reinterpret_cast<float4*>(p.o) + part * (D / 4) * kRowsOut + r;
         auto put = [&](int col, const float (&y)[32]) {
 #pragma unroll
             for (int j = 0; j < 32; j += 8) {
-                po[(col + j) / 4 * kRowsCta] = MX ? make_float4(y[j], y[j + 2], y[j + 4], y[j + 6])
+                po[(col + j) / 4 * kRowsOut] = MX ? make_float4(y[j], y[j + 2], y[j + 4], y[j + 6])
                                                   : make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-                po[((col + j) / 4 + 1) * kRowsCta] = MX ? make_float4(y[j + 1], y[j + 3], y[j + 5], y[j + 7])
+                po[((col + j) / 4 + 1) * kRowsOut] = MX ? make_float4(y[j + 1], y[j + 3], y[j + 5], y[j + 7])
                                                         : make_float4(y[j + 4], y[j + 5], y[j + 6], y[j + 7]);
             }
         };
@@ -1061,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float M = fmaxf(m_run, other.x);
             const float wa = m_run == -INFINITY ? 0.0f : ex2_approx(m_run - M);
             const float wb = other.x == -INFINITY ? 0.0f : ex2_approx(other.x - M);
-            if (g == 0) p.stat[part * 128 + r] = make_float2(M, wa * l + wb * other.y);
+            if (g == 0 && r < kRowsOut) p.stat[part * kRowsOut + r] = make_float2(M, wa * l + wb * other.y);
             if (nt > 0 && !idle) {
 #pragma unroll
                 for (int hf = 0; hf < D / 64; ++hf) {
@@ -1129,14 +1162,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 // 16-byte chunk c of the code row (V: 16 channels of a key;
                 // V^T: 16 keys of a channel) -> two chunks of the fp16 row;
-                // slots behind the prefix's end count as zeros, the others'
+                // slots without a key of the part count as zeros, the others'
                 // scales (relative to 2^vexp, rounded to fp16) are multiplied in
                 const int c8 = i % kScStages;
                 if (!warp_all(mbar_wait(&bars[Sm::kScFull + c8], (i / kScStages) & 1, abort_flag, &g_shared_err, 16))) break;
                 const uint8_t* vsc = reinterpret_cast<const uint8_t*>(scl + c8 * Sm::kScSlot + kKeys);
                 const uint32_t vs_row = p.per_tensor || p.v_trans
                                             ? 0u : 0x10001u * *reinterpret_cast<const uint16_t*>(vsc + 2 * row);
-                const int left = L - (tb + i) * kKeys;           // keys of the tile below L
+                const int left = gone - (tb + i) * kKeys, skip = OWN ? there - (tb + i) * kKeys : 0;   // keys [skip, left)
                 auto convert = [&](auto width_c, auto trans_c, int atom_b) {
                     constexpr bool kTrans = decltype(trans_c)::value;
                     constexpr int kWidth = decltype(width_c)::value;
@@ -1145,14 +1178,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kWidth / 16; ++c)
                         u[c] = *reinterpret_cast<const uint4*>(vrow + (e4m3_chunk<kWidth>(c, row) << 4));
-                    if (left < kKeys) {
+                    if (left < kKeys || (OWN && skip > 0)) {
 #pragma unroll
                         for (int c = 0; c < kWidth / 16; ++c) {
-                            const int n = kTrans ? left - 16 * c : (row < left ? 16 : 0);
-                            u[c].x &= low_bytes(n);
-                            u[c].y &= low_bytes(n - 4);
-                            u[c].z &= low_bytes(n - 8);
-                            u[c].w &= low_bytes(n - 12);
+                            const int n = kTrans ? left - 16 * c : (row < left && row >= skip ? 16 : 0);
+                            const int m = OWN && kTrans ? skip - 16 * c : 0;
+                            u[c].x &= low_bytes(n) & ~low_bytes(m);
+                            u[c].y &= low_bytes(n - 4) & ~low_bytes(m - 4);
+                            u[c].z &= low_bytes(n - 8) & ~low_bytes(m - 8);
+                            u[c].w &= low_bytes(n - 12) & ~low_bytes(m - 12);
                         }
                     }
 #pragma unroll
@@ -1202,6 +1236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (OWN) pdl_wait();                             // this grid ends after the one before it
 }
 
 // -------------------------------------------------------------- few rows
@@ -1417,7 +1452,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
         blk0 = hi >= 0 ? lo / kBlk : 0;
         n_all = hi >= 0 ? hi / kBlk + 1 - blk0 : 0;
     } else {
-        own_keys(max(0, min(ctx[0], cap)), L, p.T, p.window, lo, hi, blk0, n_all);
+        own_keys(max(0, min(ctx[0], cap)), L, p.T, p.window, 6, lo, hi, blk0, n_all);
     }
     int first, last;
     share_out(n_all, used_splits(n_all, nsplit, lg_s), split, first, last);
@@ -1861,7 +1896,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 3)
 // How a batch's work is cut, and where its pieces lie in the workspace.
 struct SharedPlan {
     int pre_rows, n_rt, np, ns;              // rows of a prefix CTA, tiles of them, their splits; a sequence's splits
-    int rows_pad;
+    int rows_pad, own_tc;                    // own_tc: a sequence's own keys by prefix_kernel too
     size_t pre_stat, pre_o, own_stat, own_o, codes, img, q_scale, bytes;
 };
 
@@ -1877,6 +1912,7 @@ SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
     w.np = (int)std::max<int64_t>(1, (few ? 2 * sms : sms) / ((int64_t)w.n_rt * Hk));
     w.ns = (int)std::max<int64_t>(1, std::min<int64_t>(32, (few ? 1 : (T * (H / Hk) > 16 ? 2 : 3)) * sms / items));
     w.rows_pad = few ? (int)rows : w.n_rt * w.pre_rows;
+    w.own_tc = 0;
     size_t at = 0;
     auto take = [&](size_t n) {
         const size_t o = at;
@@ -1936,33 +1972,41 @@ void choose_cut(const DecodeSharedArgs& sa, SharedPlan& w) {
         for (int n = 0; n < 7; ++n, per += std::max(step, per / 4 / step * step)) {
             const int np = (int)ceil_div(tiles, per);
             const float ctas = (float)units * np, tp = pre_fixed[rg] + per * tile[rg];
-            const float waves = std::ceil(ctas / sms), slots = std::max(0.0f, sms - ctas) * per_sm * beside;
-            for (int ns = 1;; ns = std::min(2 * ns, most.ns)) {
-                const int used = std::max(1, std::min(ns, (half + (1 << lg_s) - 1) >> lg_s));
-                const int least = std::min(ns, used_splits(blocks, ns, lg_s));
-                const float most_own = own_fixed + own_block * ceil_div(blocks, (int64_t)least << lg_s);
-                const float mean_own = own_fixed + own_block * ceil_div(half, (int64_t)used << lg_s);
-                const float work = (float)items * used * mean_own, rest = work - slots * tp;
-                float t = std::max(waves * tp, most_own);
-                if (ctas >= sms) t = waves * tp + std::max(work / (sms * per_sm), most_own);
-                else if (rest > 0.0f) t = std::max(tp + std::max(rest / (sms * per_sm), mean_own), most_own);
-                t += (ctas * 128 * rg + (float)items * used * R) * a.D * 4 / merge_bytes;
-                if (t < best) {
-                    best = t;
-                    w.pre_rows = 128 * rg;
-                    w.n_rt = (int)(units / a.Hk);
-                    w.np = np;
-                    w.ns = ns;
-                    w.rows_pad = w.n_rt * w.pre_rows;
+            const float waves = std::ceil(ctas / sms);
+            // own keys by rows_kernel, or by prefix_kernel (one CTA an SM, as
+            // many 128-key tiles as half the 64-key blocks)
+            for (int v = 0; v < (R > 32 ? 2 : 1); ++v) {
+                const int lg = v ? 1 : lg_s, units_max = v ? (blocks + 1) / 2 + 1 : blocks, units_mean = std::max(1, v ? (half + 1) / 2 : half);
+                const int fit = v ? 1 : per_sm;
+                const float slots = std::max(0.0f, sms - ctas) * fit * (v ? 0.9f : beside);
+                const float fixed = v ? pre_fixed[1] : own_fixed, block = v ? 2.0f * tile[1] : own_block;
+                for (int ns = 1;; ns = std::min(2 * ns, most.ns)) {
+                    const int used = used_splits(units_mean, ns, lg), least = used_splits(units_max, ns, lg);
+                    const float most_own = fixed + block * ceil_div(units_max, (int64_t)least << lg);
+                    const float mean_own = fixed + block * ceil_div(units_mean, (int64_t)used << lg);
+                    const float work = (float)items * used * mean_own, rest = work - slots * tp;
+                    float t = std::max(waves * tp, most_own);
+                    if (ctas >= sms) t = waves * tp + std::max(work / (sms * fit), most_own);
+                    else if (rest > 0.0f) t = std::max(tp + std::max(rest / (sms * fit), mean_own), most_own);
+                    t += (ctas * 128 * rg + (float)items * used * R) * a.D * 4 / merge_bytes;
+                    if (t < best) {
+                        best = t;
+                        w.pre_rows = 128 * rg;
+                        w.n_rt = (int)(units / a.Hk);
+                        w.np = np;
+                        w.ns = ns;
+                        w.own_tc = v;
+                        w.rows_pad = w.n_rt * w.pre_rows;
+                    }
+                    if (ns == most.ns) break;
                 }
-                if (ns == most.ns) break;
             }
             if (np == 1) break;
         }
     }
 }
 
-template <int D, bool MX, int RG>
+template <int D, bool MX, int RG, bool OWN>
 cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, const CUtensorMap& tk, const CUtensorMap& tv,
                           cudaStream_t s) {
     const DecodeArgs& a = sa.d;
@@ -1977,7 +2021,10 @@ cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, const
     p.v_trans = (!MX && (a.kv_flags & 2)) ? 1 : 0;
     p.ksf8 = a.k_sf;
     p.vsf8 = a.v_sf;
-    p.ptab = sa.prefix_table;
+    p.codes = ws + w.codes;
+    p.rows_pad = w.rows_pad;
+    p.max_pages = a.max_pages;
+    p.ptab = OWN ? a.page_table : sa.prefix_table;
     p.plen = sa.prefix_len;
     p.ctx = a.ctx_lens;
     p.T = a.T;
@@ -1992,14 +2039,14 @@ cudaError_t launch_prefix(const DecodeSharedArgs& sa, const SharedPlan& w, const
     p.cap_rows = a.max_pages * a.page_size;
     p.num_pages = a.num_pages;
     p.window = std::min(a.window, INT32_MAX - 64);           // (positions start at -T: no wrap)
-    p.np = w.np;
+    p.np = OWN ? w.ns : w.np;
     p.n_rt = w.n_rt;
     p.logit_scale_log2 = a.softmax_scale / static_cast<float>(D) * kLog2e;
-    p.stat = reinterpret_cast<float2*>(ws + w.pre_stat);
-    p.o = reinterpret_cast<float*>(ws + w.pre_o);
-    const cudaError_t e = allow_smem<prefix_kernel<D, MX, RG>>(kSmem);
+    p.stat = reinterpret_cast<float2*>(ws + (OWN ? w.own_stat : w.pre_stat));
+    p.o = reinterpret_cast<float*>(ws + (OWN ? w.own_o : w.pre_o));
+    const cudaError_t e = allow_smem<prefix_kernel<D, MX, RG, OWN>>(kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(prefix_kernel<D, MX, RG>, dim3(w.np, w.n_rt * a.Hk), dim3(kThreads), kSmem, s, tk, tv, p);
+    return launch_pdl(prefix_kernel<D, MX, RG, OWN>, OWN ? dim3(w.ns, a.B * a.Hk) : dim3(w.np, w.n_rt * a.Hk), dim3(kThreads), kSmem, s, tk, tv, p);
 }
 
 template <int D, bool MX>
@@ -2046,7 +2093,8 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     if (!ok) return cudaErrorInvalidValue;
     if (!few) {
         const CUtensorMap& tvp = vt ? tv128 : tv;
-        e = w.pre_rows == 128 ? launch_prefix<D, MX, 1>(sa, w, tk, tvp, s) : launch_prefix<D, MX, 2>(sa, w, tk, tvp, s);
+        e = w.pre_rows == 128 ? launch_prefix<D, MX, 1, false>(sa, w, tk, tvp, s) : launch_prefix<D, MX, 2, false>(sa, w, tk, tvp, s);
+        if (e == cudaSuccess && w.own_tc) e = launch_prefix<D, MX, 1, true>(sa, w, tk, tvp, s);
         if (e != cudaSuccess) return e;
     }
     RowsParams r = {};
@@ -2094,7 +2142,9 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     r.div_g = fast_div_by(r.G);
     const dim3 grid((unsigned)(r.np * a.Hk + (int64_t)w.ns * a.B * a.Hk)), block(32 * kRowsWarps);
     const int mts = (int)ceil_div(few ? q.n_rows : q.R, 16);
-    if (vt) {
+    if (w.own_tc) {
+        // (launched above)
+    } else if (vt) {
         using Sm = SmR<D, false, true>;
         e = allow_smem<rows_kernel<D, false, true>>(Sm::bytes(4));
         if (e == cudaSuccess) e = launch_pdl(rows_kernel<D, false, true>, grid, block, Sm::bytes(mts), s, tk, tv, r);
@@ -2130,7 +2180,8 @@ cudaError_t launch_shared_d(const DecodeSharedArgs& sa, cudaStream_t s) {
     m.ctx = a.ctx_lens;
     m.cap_rows = a.max_pages * a.page_size;
     m.window = r.window;
-    m.lg_own = lg_slices(q.R);
+    m.lg_unit = w.own_tc ? 7 : 6;
+    m.lg_own = w.own_tc ? 1 : lg_slices(q.R);
     // (four warps hold all of sixteen parts at once)
     const dim3 mg((unsigned)ceil_div(m.n_rows, 32), D / kCh, a.Hk);
     return w.np + w.ns <= 16 ? launch_pdl(shared_merge_kernel<D, 4>, mg, dim3(128), 0, s, m)

@@ -471,6 +471,36 @@ def test_shared_reports_bad_pages_and_lengths(handles):
     assert sage.sage_device_error() == sage.SAGE_OK
 
 
+@pytest.mark.parametrize("B,T,H,Hk,D,page,prefix,lo,hi,window,fmt,poison", [
+    (16, 4, 16, 1, 128, 128, 500, 4, 2100, 10 ** 6, "token", True), (16, 4, 16, 1, 128, 16, 300, 4, 1500, 900, "token", True),
+    (12, 3, 24, 2, 64, 32, 77, 3, 1300, 10 ** 6, "tensor", True), (12, 4, 32, 2, 64, 128, 130, 1, 1300, 700, "token_vt", True),
+    (16, 4, 16, 1, 128, 128, 257, 4, 1800, 10 ** 6, "tensor_vt", True), (14, 3, 12, 1, 128, 64, 129, 0, 1500, 10 ** 6, "mxfp4", False),
+    (16, 4, 16, 1, 128, 16, 40, 4, 1500, 400, "mxfp4", False),
+])
+def test_shared_many_rows_and_long_own_keys(handles, B, T, H, Hk, D, page, prefix, lo, hi, window, fmt, poison):
+    """36 to 64 rows a sequence and hundreds to thousands of own keys each, of
+    very different lengths; NaN codes wherever no key is."""
+    rng = np.random.default_rng(B + prefix + hi)
+    ctx = [int(prefix + rng.integers(lo, hi)) for _ in range(B)]
+    ctx[0], ctx[1], ctx[2], ctx[3] = prefix + hi, prefix + 1, prefix, 0
+    d = sh.make_shared(B, T, H, Hk, D, page, prefix, ctx, seed=B + hi, fmt=fmt)
+    if poison:
+        used = np.zeros((d["pages"], page), bool)
+        for b in range(B):
+            for j in range(ctx[b]):
+                used[d["prefix"][j // page] if j < prefix else d["table"][b, j // page], j % page] = True
+        dead = torch.from_numpy(~used)
+        for n in ("k", "v"):
+            c = d[n + "c"].transpose(2, 3) if n == "v" and fmt.endswith("vt") else d[n + "c"]
+            c.copy_(torch.where(dead[:, None, :, None], torch.tensor(127, dtype=torch.uint8), c))
+            if not fmt.startswith("tensor"):
+                d[n + "s"] = torch.where(dead[:, None, :], float("nan"), d[n + "s"])
+    out = run_shared(handles[D], d, page, window, 1.0 / math.sqrt(D))
+    torch.cuda.synchronize()
+    assert sage.sage_device_error() == sage.SAGE_OK
+    check_shared(out, d, window, 1.0 / math.sqrt(D))
+
+
 @pytest.mark.parametrize("seed", range(32))
 def test_shared_random_shapes(handles, seed):
     """Sizes drawn over what the interface takes: row counts on both sides of
