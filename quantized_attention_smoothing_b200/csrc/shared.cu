@@ -1935,16 +1935,17 @@ SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
 }
 
 // The cut of a call, by its estimated time. A prefix CTA has an SM to itself;
-// the sequences' own CTAs run on the SMs left over, or behind it, and 128 or
-// 256 rows a CTA trade partials for conversions of V, so the most CTAs are not
-// the least time: MXFP4 B32 behind 16384 tokens takes 37.8 us with 128 prefix
-// CTAs of two tiles and 27.9 us with 86 of three, B16 T4 window 4096 36.8 and
-// 30.6. The model's constants (microseconds; tiles are 128 keys, blocks 64
-// keys a warp) are fitted to 44 batches of 65 to 4096 rows over all their cuts:
-// its choice is 1.5 % slower than the best one on average, 10 % at worst. The
-// lengths are on the device; the tables' sizes stand for them, and a sequence's
-// own keys for half of what its table has room for (only the time depends on
-// that).
+// the sequences' own CTAs run on the SMs left over, or behind it; 128 or 256
+// rows a CTA trade partials for conversions of V; and the own keys of sequences
+// of many rows may go to prefix_kernel too. So the most CTAs are not the least
+// time: MXFP4 B32 behind 16384 tokens takes 37.8 us with 128 prefix CTAs of two
+// tiles and 27.8 with 86 of three; B16 T4 window 4096 36.8 with 64 + 256 CTAs,
+// 30.1 with 16 + 256, and 24.1 with 32 + 64, own keys by prefix_kernel. The
+// model's constants (microseconds; tiles are 128 keys, blocks 64 keys a warp)
+// are fitted to 70 batches of 65 to 4096 rows over all their cuts: its choice
+// is 2 % slower than the best one on average, 29 % at worst. The lengths are on
+// the device; the tables' sizes stand for them, and a sequence's own keys for
+// half of what its table has room for (only the time depends on that).
 void choose_cut(const DecodeSharedArgs& sa, SharedPlan& w) {
     const DecodeArgs& a = sa.d;
     const int sms = device_sms(), R = a.T * (a.H / a.Hk), lg_s = lg_slices(R), per_sm = R > 16 ? 2 : 3;
@@ -1959,9 +1960,16 @@ void choose_cut(const DecodeSharedArgs& sa, SharedPlan& w) {
     const int tiles = (int)std::max<int64_t>(1, std::min(ceil_div(cap_pre, kKeys), ceil_div(seen, kKeys) + 1));
     const int blocks = (int)ceil_div(std::max<int64_t>(kBlk, std::min(cap_row - cap_pre + a.page_size, seen)), kBlk);
     const int half = std::max(1, blocks / 2);                              // of an average sequence
-    const float pre_fixed[3] = {0.0f, 5.3f, 6.3f}, tile[3] = {0.0f, a.mx ? 2.3f : 1.45f, a.mx ? 3.6f : 2.75f};
-    const float own_fixed = 5.4f, own_block = a.mx ? 4.0f : 2.0f;
-    const float beside = 0.6f, merge_bytes = 6.9e6f;                       // share of the SMs left over; bytes a us
+    const float d64 = a.D == 64 ? 0.7f : 1.0f;
+    const float pre_fixed[3] = {0.0f, 4.1f, 6.4f}, tile[3] = {0.0f, a.mx ? 2.75f : 1.48f * d64, a.mx ? 3.37f : 1.79f * d64};
+    const float merge_bytes = 3.5e6f;                                      // a microsecond
+    // own keys by rows_kernel, by prefix_kernel: a CTA, a block (tile); CTAs an
+    // SM; the share of the SMs left over that they get beside the prefix
+    const float own_fixed[2] = {2.8f, 5.8f};
+    const float own_unit[2] = {(a.mx ? 5.56f : 2.16f * d64) * (R > 16 ? 0.84f : 1.0f), 2.0f * (a.mx ? 1.95f : 1.03f * d64)};
+    const int fit[2] = {per_sm, 1};
+    const float beside[2] = {0.34f, 0.2f};
+    const float whole = 0.53f;                                             // of a last wave that is not full
     const SharedPlan most = w;
     float best = FLT_MAX;
     for (int rg = rows <= 128 ? 1 : 2; rg >= 1; --rg) {
@@ -1973,22 +1981,23 @@ void choose_cut(const DecodeSharedArgs& sa, SharedPlan& w) {
             const int np = (int)ceil_div(tiles, per);
             const float ctas = (float)units * np, tp = pre_fixed[rg] + per * tile[rg];
             const float waves = std::ceil(ctas / sms);
-            // own keys by rows_kernel, or by prefix_kernel (one CTA an SM, as
-            // many 128-key tiles as half the 64-key blocks)
             for (int v = 0; v < (R > 32 ? 2 : 1); ++v) {
                 const int lg = v ? 1 : lg_s, units_max = v ? (blocks + 1) / 2 + 1 : blocks, units_mean = std::max(1, v ? (half + 1) / 2 : half);
-                const int fit = v ? 1 : per_sm;
-                const float slots = std::max(0.0f, sms - ctas) * fit * (v ? 0.9f : beside);
-                const float fixed = v ? pre_fixed[1] : own_fixed, block = v ? 2.0f * tile[1] : own_block;
+                const float slots = std::max(0.0f, sms - ctas) * fit[v], all = (float)sms * fit[v];
                 for (int ns = 1;; ns = std::min(2 * ns, most.ns)) {
                     const int used = used_splits(units_mean, ns, lg), least = used_splits(units_max, ns, lg);
-                    const float most_own = fixed + block * ceil_div(units_max, (int64_t)least << lg);
-                    const float mean_own = fixed + block * ceil_div(units_mean, (int64_t)used << lg);
-                    const float work = (float)items * used * mean_own, rest = work - slots * tp;
-                    float t = std::max(waves * tp, most_own);
-                    if (ctas >= sms) t = waves * tp + std::max(work / (sms * fit), most_own);
-                    else if (rest > 0.0f) t = std::max(tp + std::max(rest / (sms * fit), mean_own), most_own);
-                    t += (ctas * 128 * rg + (float)items * used * R) * a.D * 4 / merge_bytes;
+                    const float longest = own_fixed[v] + own_unit[v] * ceil_div(units_max, (int64_t)least << lg);
+                    const float mean = own_fixed[v] + own_unit[v] * ceil_div(units_mean, (int64_t)used << lg);
+                    const float n_own = (float)items * used;
+                    auto run = [&](float n) { return mean * (std::ceil(n / all) * whole + n / all * (1.0f - whole)); };
+                    float t = std::max(waves * tp, longest);
+                    if (ctas >= sms) {
+                        t = waves * tp + std::max(run(n_own), longest);
+                    } else if (n_own > slots) {
+                        const float done = (std::floor(tp / mean) * whole + tp / mean * (1.0f - whole)) * slots * beside[v];
+                        if (n_own > done) t = std::max(tp + std::max(mean, run(n_own - done)), longest);
+                    }
+                    t += (ctas * 128 * rg + n_own * R) * a.D * 4 / merge_bytes;
                     if (t < best) {
                         best = t;
                         w.pre_rows = 128 * rg;
