@@ -1922,14 +1922,14 @@ SharedPlan shared_plan(int B, int T, int H, int Hk, int D) {
     // (in 128-row CTAs no more than in 256-row ones: at most one an SM, or one
     // a row tile)
     const size_t pre = std::max<size_t>((size_t)w.n_rt * Hk * w.np, few ? 0 : sms) * w.pre_rows, own = (size_t)items * w.ns * 64;
-    const size_t q_rows = (size_t)Hk * w.rows_pad;
+    const size_t q_rows = (size_t)Hk * (few ? 128 : w.rows_pad);    // (up to 64 rows may go to prefix_kernel too)
     w.pre_stat = take(pre * sizeof(float2));
     w.own_stat = take(own * sizeof(float2));
     w.pre_o = take(pre * D * sizeof(float));
     w.own_o = take(own * D * sizeof(float));
-    w.codes = take(few ? 0 : q_rows * D);
-    w.img = take(few ? 0 : q_rows * 2 * D);                  // (bf16 images for an MXFP4 cache)
-    w.q_scale = take(few ? 0 : q_rows * sizeof(float));
+    w.codes = take(q_rows * D);
+    w.img = take(q_rows * 2 * D);                            // (bf16 images for an MXFP4 cache)
+    w.q_scale = take(q_rows * sizeof(float));
     w.bytes = at;
     return w;
 }
@@ -1952,11 +1952,6 @@ void choose_cut(const DecodeSharedArgs& sa, SharedPlan& w) {
     const int64_t rows = (int64_t)a.B * R, items = (int64_t)a.B * a.Hk;
     const int64_t cap_pre = (int64_t)sa.max_prefix_pages * a.page_size, cap_row = (int64_t)a.max_pages * a.page_size;
     const int64_t seen = std::min<int64_t>(cap_row, (int64_t)a.window + a.T);
-    if (w.pre_rows == kFewRows) {
-        w.np = used_splits((int)ceil_div(cap_pre, kBlk), w.np, lg_slices((int)rows));
-        w.ns = used_splits((int)ceil_div(cap_row, kBlk), w.ns, lg_s);
-        return;
-    }
     const int tiles = (int)std::max<int64_t>(1, std::min(ceil_div(cap_pre, kKeys), ceil_div(seen, kKeys) + 1));
     const int blocks = (int)ceil_div(std::max<int64_t>(kBlk, std::min(cap_row - cap_pre + a.page_size, seen)), kBlk);
     const int half = std::max(1, blocks / 2);                              // of an average sequence
@@ -1972,9 +1967,21 @@ void choose_cut(const DecodeSharedArgs& sa, SharedPlan& w) {
     const float whole = 0.53f;                                             // of a last wave that is not full
     const SharedPlan most = w;
     float best = FLT_MAX;
+    if (w.pre_rows == kFewRows) {
+        // rows_kernel for both parts, one launch fewer. With over 16 rows a
+        // block costs twice what it does beside a prefix (64 rows behind 29932
+        // tokens, 8 heads of 64: 51.8 us, 32.1 by prefix_kernel), but a call of one
+        // block a warp is 3.5 us shorter (9.2 against 12.6).
+        const int lg = lg_slices((int)rows);
+        w.np = used_splits((int)ceil_div(cap_pre, kBlk), w.np, lg);
+        w.ns = used_splits((int)ceil_div(cap_row, kBlk), w.ns, lg_s);
+        if (rows <= 16) return;
+        const int64_t pre_blocks = std::min(ceil_div(cap_pre, kBlk), ceil_div(seen, kBlk) + 1);
+        best = (a.mx ? 6.0f : 3.6f) * ceil_div(pre_blocks, (int64_t)w.np << lg) - 1.5f;
+    }
     for (int rg = rows <= 128 ? 1 : 2; rg >= 1; --rg) {
         const int64_t units = ceil_div(rows, 128 * rg) * a.Hk;            // row tiles of all heads
-        if (rg == 1 && most.pre_rows == 256 && units > sms) continue;      // (the layout's bound)
+        if (rg == 1 && most.pre_rows != 128 && units > sms) continue;      // (the layout's bound)
         const int np_max = (int)std::max<int64_t>(1, sms / units), step = rg == 1 ? 2 : 1;
         int per = (int)ceil_div(std::max(ceil_div(tiles, np_max), (int64_t)step), step) * step;
         for (int n = 0; n < 7; ++n, per += std::max(step, per / 4 / step * step)) {

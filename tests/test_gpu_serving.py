@@ -501,6 +501,23 @@ def test_shared_many_rows_and_long_own_keys(handles, B, T, H, Hk, D, page, prefi
     check_shared(out, d, window, 1.0 / math.sqrt(D))
 
 
+@pytest.mark.parametrize("B,T,H,Hk,D,page,prefix,fmt", [
+    (4, 1, 128, 8, 64, 16, 7990, "token"), (1, 4, 128, 8, 128, 128, 8100, "tensor_vt"), (3, 2, 80, 8, 128, 32, 8077, "mxfp4"),
+    (17, 1, 8, 8, 128, 64, 8000, "token"),
+])
+def test_shared_few_rows_behind_a_long_prefix(handles, B, T, H, Hk, D, page, prefix, fmt):
+    """17 to 64 rows a head and many key tiles a split, where either kernel may
+    take the prefix; one sequence ends inside it."""
+    ctx = [prefix + 5 + 40 * b for b in range(B)]
+    ctx[-1] = prefix // 2 if B > 1 else ctx[-1]
+    d = sh.make_shared(B, T, H, Hk, D, page, prefix, ctx, seed=B + H, fmt=fmt)
+    for window in (10 ** 6, 3000):
+        out = run_shared(handles[D], d, page, window, 1.0 / math.sqrt(D))
+        torch.cuda.synchronize()
+        assert sage.sage_device_error() == sage.SAGE_OK
+        check_shared(out, d, window, 1.0 / math.sqrt(D))
+
+
 @pytest.mark.parametrize("seed", range(32))
 def test_shared_random_shapes(handles, seed):
     """Sizes drawn over what the interface takes: row counts on both sides of
