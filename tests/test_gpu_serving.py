@@ -717,3 +717,55 @@ def test_serving_loop(handles, fmt, page, Hk, side):
         assert np.mean(have != want) < 1e-3               # signed zeros
     else:
         assert not ((have != want) & ((have & 127) != 0)).any()
+
+
+@pytest.mark.parametrize("B,T,G,fmt", [(40, 1, 16, "token"), (3, 2, 4, "token"), (9, 3, 16, "mxfp4")])
+def test_serving_steps_without_waiting(handles, B, T, G, fmt):
+    """Steps issued back to back, where a kernel may start before the one before
+    it has ended: every step's output is the one that the same steps give with
+    the GPU waited for after every call."""
+    D, Hk, page, P, mp, steps = 128, 2, 32, 70, 16, 40
+    h, H, mx = handles[D], G * Hk, fmt == "mxfp4"
+    pages = B * mp + 8
+    g = torch.Generator().manual_seed(3)
+    mean = torch.randn((Hk, D), generator=g).cuda()
+    kv = [torch.randn((max(B * T, P), 2 * Hk, D), generator=g).to(torch.bfloat16).cuda() for _ in range(steps + 1)]
+    q = [torch.randn((B, T, H, D), generator=g).to(torch.bfloat16).cuda() for _ in range(steps)]
+    perm = torch.randperm(pages, generator=g).int()
+    new = torch.full((B,), T, dtype=torch.int32).cuda()
+    length = dev([2 * page])
+
+    def run(wait):
+        shape = (pages, Hk, page, D // 2 if mx else D)
+        kc, vc = (torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2))
+        ks, vs = (torch.zeros((pages, Hk, page) + ((D // 32,) if mx else ()), dtype=torch.uint8 if mx else torch.float32,
+                              device="cuda") for _ in range(2))
+        prefix, free = perm[:2].cuda(), torch.cat((perm[2:], perm[:2])).cuda()
+        cached, count = dev(np.zeros(B)), dev([pages - 2])
+        table, off, slots = dev(np.zeros((B, mp))), dev(np.zeros(B + 1)), dev(np.zeros(B * T))
+        ws = torch.empty((sage.sage_attn_decode_shared_workspace(B, T, H, Hk, D),), dtype=torch.uint8, device="cuda")
+        outs = [torch.zeros_like(x) for x in q]
+        fill = (prefix[:, None] * page + torch.arange(page, device="cuda")[None]).reshape(-1).int()
+        append = sage.sage_kv_append_mxfp4 if mx else sage.sage_kv_append
+        attend = sage.sage_attn_decode_shared_mxfp4 if mx else sage.sage_attn_decode_shared
+        x = kv[steps][:2 * page]
+        append(h, x[:, :Hk], x[:, Hk:], fill, kc, vc, ks, vs, k_mean=mean)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            x = kv[i][:B * T]
+            sage.sage_page_plan(cached, new, free, count, page, table, cached, count, off, slots, prefix_table=prefix)
+            if wait:
+                torch.cuda.synchronize()
+            append(h, x[:, :Hk], x[:, Hk:], slots, kc, vc, ks, vs, k_mean=mean)
+            if wait:
+                torch.cuda.synchronize()
+            attend(h, q[i], kc, vc, ks, vs, prefix, length, table, cached, page, pages, 10 ** 6, 0.09, outs[i], ws)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert sage.sage_device_error() == sage.SAGE_OK
+        return outs
+    want, got = run(True), run(False)
+    assert all(torch.isfinite(x).all() for x in want)
+    for i in range(steps):
+        assert torch.equal(want[i], got[i]), i
