@@ -557,6 +557,25 @@ def test_shared_value_scales_far_apart(handles, B, prefix, ctx):
     check_shared(out, d, 9999, 0.09)
 
 
+@pytest.mark.parametrize("B,T,H,prefix,ctx,fmt", [
+    (9, 1, 16, 700, [700 + 30 * b for b in range(9)], "token"), (1, 2, 8, 300, [700], "token"),
+    (16, 4, 16, 130, [130 + 100 * b for b in range(16)], "token"), (9, 1, 16, 700, [700 + 30 * b for b in range(9)], "token_vt"),
+])
+def test_shared_tokens_of_zeros(handles, B, T, H, prefix, ctx, fmt):
+    """Keys and values of zeros (scale 0, as the cache write leaves them): whole
+    first tiles of them, then single ones; and queries of zeros."""
+    d = sh.make_shared(B, T, H, 1, 128, 128, prefix, ctx, seed=B + T, fmt=fmt)
+    first = [int(d["prefix"][0]), int(d["prefix"][1])] + [int(x) for x in d["table"][:, prefix // 128] if x < 1 << 20]
+    for n in ("ks", "vs"):
+        d[n][first] = 0.0
+        d[n][:, :, 5::17] = 0.0
+    d["q"][0, 0, 1] = 0
+    out = run_shared(handles[128], d, 128, 9999, 0.09)
+    check_shared(out, d, 9999, 0.09)
+    d["vs"].zero_()
+    assert not run_shared(handles[128], d, 128, 9999, 0.09).any()
+
+
 def test_shared_and_append_far_into_a_large_cache(handles):
     """Caches of over 2^32 bytes: pages at their far end give the same bits as
     the same pages in a small cache, for reading and for writing."""
