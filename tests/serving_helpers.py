@@ -157,8 +157,9 @@ def cache_values(d, n):
 
 def ref_shared(d, window, scale):
     """(out, tol) fp64 [B, T, H, D]. The kernels hold S, the softmax statistics
-    and O in fp32 and round twice to bf16: every weight (times its value scale)
-    and the output, each by at most half a step, 2^-8 of the value. Logits are
+    and O in fp32 and round twice: every product of a weight and a value (to
+    bf16, at most half a step, 2^-8 of it; or in fp16 the weight, the value's
+    scale and the scaled value, 3 times 2^-11) and the output (2^-8). Logits are
     fp32 sums of 128 exact products: an error of 2^-17 of sum |q k| each, and
     2^-20 for their scaling and the exponential, which moves a weight and the
     denominator by as much. So |error| <= (2^-8 + 2 e) sum p |v| + 2^-8 |y|."""
