@@ -400,9 +400,14 @@ constexpr int kRegsSoft = 168, kRegsConv = 96, kRegsProd = 80;
 static_assert(256 * kRegsSoft + 128 * kRegsConv + 128 * kRegsProd <= kThreads * 128, "register split");
 // A unit's 64 weights against the running max: where they add up to more than
 // kMaxSum some logit is over 2 above it, and the max is raised wherever that is
-// so (kRaise); where a row's first ones add up to less than kMinSum they have
-// lost bits, or vanished, and its max is taken first.
-constexpr float kMaxSum = 256.0f, kRaise = 2.0f, kMinSum = 0x1p-54f;
+// so (kRaise); where a row's first ones add up to less than kMinSum its max is
+// taken first. The sum l keeps the fp32 weights, so the 16-bit ones must not
+// lose bits beside it: fp16 (FP8 cache) holds 2^-24 at least, so the first
+// unit's have to add up to 1 (the largest is then 2^-6 or more, and no weight
+// is off by more than 2^-25 of l); bf16 (MXFP4) has the range of fp32.
+constexpr float kMaxSum = 256.0f, kRaise = 2.0f;
+template <bool MX>
+constexpr float kMinSum = MX ? 0x1p-54f : 1.0f;
 // one pair of exponentials in 2 kPolyEvery goes to the FMA pipe
 constexpr int kPolyEvery = 4;
 
@@ -940,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float a, b;
                     f2_unpack(lsum, a, b);
                     a += b;
-                    slow = __any_sync(0xffffffffu, all && (a > kMaxSum || (l2 == 0 && a < kMinSum)));
+                    slow = __any_sync(0xffffffffu, all && (a > kMaxSum || (l2 == 0 && a < kMinSum<MX>)));
                     if (!slow) {
                         if (__any_sync(0xffffffffu, none)) {
 #pragma unroll
