@@ -297,6 +297,18 @@ def sage_attn_fwd(q8, q_scale, k8, k_scale, v8_t, v_scale, B, H, Hk, Lq, Lk, D, 
                                _stream(stream)), "sage_attn_fwd")
 
 
+def _workspace(nbytes, device, stream):
+    """A workspace for one call on `stream`, allocated under that stream: it is
+    released when the call returns, and its memory then goes to work that
+    follows the call's kernels on the same stream."""
+    if stream is None:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty((nbytes,), dtype=torch.uint8, device=device)
+
+
 def sage_attn_decode(h, q, k_cache, v_cache, k_scale, v_scale, page_table, ctx_lens, page_size,
                      num_pages, window, softmax_scale, out, ws=None, stream=None, q8_out=None,
                      q_scale_out=None, kv_flags=0):
@@ -308,7 +320,7 @@ def sage_attn_decode(h, q, k_cache, v_cache, k_scale, v_scale, page_table, ctx_l
         # one CTA)
         n = sage_attn_decode_workspace(B, T, H, Hk, D, window)
         if n > 0:
-            ws = torch.empty((n,), dtype=torch.uint8, device=q.device)
+            ws = _workspace(n, q.device, stream)
     _check(lib().sage_attn_decode(h.handle, _view(q, CView4), _ptr(k_cache), _ptr(v_cache),
                                   _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(ctx_lens),
                                   B, T, H, Hk, D, int(page_size), int(max_pages), int(num_pages),
@@ -330,7 +342,7 @@ def sage_attn_decode_mxfp4(h, q, k_cache, v_cache, k_sf, v_sf, page_table, ctx_l
     if ws is None:
         n = sage_attn_decode_workspace(B, T, H, Hk, D, window)
         if n > 0:
-            ws = torch.empty((n,), dtype=torch.uint8, device=q.device)
+            ws = _workspace(n, q.device, stream)
     _check(lib().sage_attn_decode_mxfp4(h.handle, _view(q, CView4), _ptr(k_cache), _ptr(v_cache),
                                         _ptr(k_sf), _ptr(v_sf), _ptr(page_table), _ptr(ctx_lens),
                                         B, T, H, Hk, D, int(page_size), int(max_pages), int(num_pages),
@@ -344,11 +356,10 @@ def sage_attn_decode_shared_workspace(B, T, H, Hk, D):
     return int(lib().sage_attn_decode_shared_workspace(B, T, H, Hk, D))
 
 
-def _shared_ws(q, Hk, ws):
+def _shared_ws(q, Hk, ws, stream):
     if ws is None:
         B, T, H, D = q.shape
-        ws = torch.empty((sage_attn_decode_shared_workspace(B, T, H, Hk, D),), dtype=torch.uint8,
-                         device=q.device)
+        ws = _workspace(sage_attn_decode_shared_workspace(B, T, H, Hk, D), q.device, stream)
     return ws
 
 
@@ -361,7 +372,7 @@ def sage_attn_decode_shared(h, q, k_cache, v_cache, k_scale, v_scale, prefix_tab
     count from the sequence's first token as in sage_attn_decode."""
     B, T, H, D = q.shape
     Hk = k_cache.shape[1]
-    ws = _shared_ws(q, Hk, ws)
+    ws = _shared_ws(q, Hk, ws, stream)
     _check(lib().sage_attn_decode_shared(h.handle, _view(q, CView4), _ptr(k_cache), _ptr(v_cache),
                                          _ptr(k_scale), _ptr(v_scale), _ptr(prefix_table),
                                          prefix_table.numel(), _ptr(prefix_len), _ptr(page_table),
@@ -379,7 +390,7 @@ def sage_attn_decode_shared_mxfp4(h, q, k_cache, v_cache, k_sf, v_sf, prefix_tab
     sage_attn_decode_mxfp4)."""
     B, T, H, D = q.shape
     Hk = k_cache.shape[1]
-    ws = _shared_ws(q, Hk, ws)
+    ws = _shared_ws(q, Hk, ws, stream)
     _check(lib().sage_attn_decode_shared_mxfp4(h.handle, _view(q, CView4), _ptr(k_cache), _ptr(v_cache),
                                                _ptr(k_sf), _ptr(v_sf), _ptr(prefix_table),
                                                prefix_table.numel(), _ptr(prefix_len), _ptr(page_table),
