@@ -21,7 +21,6 @@
 // V of a row are loaded together before either is used. (With 32 consecutive
 // elements a thread, 16-byte accesses 64 bytes apart, 32760 tokens of 8 heads
 // took 74.5 us, 2.7 TB/s.)
-#include <cfloat>
 #include <cstdint>
 
 #include <cuda.h>
@@ -90,11 +89,6 @@ __device__ __forceinline__ uint2 codes_e4m3(const uint64_t (&x)[4], float r) {
                (static_cast<uint32_t>(e4m3x2_rn_satfinite(p2lo(b), p2hi(b))) << 16);
     }
     return make_uint2(w[0], w[1]);
-}
-
-// 448 / a, kept finite where a is so small that the quotient is not.
-__device__ __forceinline__ float inv_scale(float a) {
-    return a != 0.0f ? fminf(__fdiv_rn(448.0f, a), FLT_MAX) : 0.0f;
 }
 
 // Eight E2M1 codes of an MX block whose largest value is a; sf: its e8m0 byte.
@@ -202,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 10) append_kernel(const AppendParams
                 float a = fmaxf(amax8(x[0]), amax8(x[1]));
 #pragma unroll
                 for (int st = 1; st < LP; st <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, st));
-                r = inv_scale(a);
+                r = e4m3_inv_scale(a);
                 if (ok && q == 0) (kv == 0 ? p.ksc : p.vsc)[tok] = __fdiv_rn(a, 448.0f);
             }
 #pragma unroll

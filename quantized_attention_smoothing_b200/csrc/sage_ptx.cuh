@@ -3,6 +3,7 @@
 // fences) and the e4m3 pair conversion. Internal to libsage.
 #pragma once
 
+#include <cfloat>
 #include <cstdint>
 #include <cuda.h>
 
@@ -456,6 +457,12 @@ __device__ __forceinline__ float2 dsmem_ld_f32x2(uint32_t addr) {
 }
 
 // ------------------------------------------------------------ numerics
+
+// 448 / a, kept finite where a is so small that the quotient is not (0 for a
+// = 0): an element of zero times an infinite quotient would be a NaN code.
+__device__ __forceinline__ float e4m3_inv_scale(float a) {
+    return a != 0.0f ? fminf(__fdiv_rn(448.0f, a), FLT_MAX) : 0.0f;
+}
 
 // Two fp32 -> packed e4m3 pair, round to nearest even, saturating to +-448
 // (OCP e4m3fn). Result byte 0 = lo, byte 1 = hi.

@@ -322,7 +322,7 @@ __device__ __forceinline__ float quantise_quarter(const uint16_t* src, int64_t s
     for (int d = 0; d < kQe; ++d) amax = fmaxf(amax, fabsf(x[d]));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const float rr = amax != 0.0f ? __fdiv_rn(448.0f, amax) : 0.0f;
+    const float rr = e4m3_inv_scale(amax);
 #pragma unroll
     for (int e = 0; e < D / 16; ++e) {
         const uint32_t lo16 = e4m3x2_rn_satfinite(__fmul_rn(x[4 * e], rr), __fmul_rn(x[4 * e + 1], rr));

@@ -96,3 +96,20 @@ def test_shared_within_the_roundings_of_its_format(handles, path, fmt, D, spread
     worst, _ = worst_error(run(handles[D], d, page, 10 ** 6, scale), d, 10 ** 6, scale)
     print("worst error %.3f of the bound" % worst)
     assert worst <= 1.0
+
+
+@pytest.mark.parametrize("fmt", ["token", "mxfp4"])
+@pytest.mark.parametrize("path", ["few rows", "rows96", "rows256"])
+def test_shared_queries_near_the_smallest_number(handles, path, fmt):
+    """Query rows whose largest rotated element is so small that 448 divided by
+    it is not a finite fp32, with elements of zero beside it: logits of zero,
+    the mean of the values that the row sees."""
+    p, D, page = PATHS[path], 128, 64
+    d = sh.make_shared(p["B"], p["T"], p["H"], p["Hk"], D, page, p["prefix"], p["ctx"], seed=2, fmt=fmt)
+    rows = d["q"].view(-1, D)
+    rows[::3] = 0
+    rows[::3, :2] = 2.0 ** -126                          # rotated: 2^-125 and 0, alternating
+    rows[3, :2] = 2.0 ** -133                            # (bf16's own subnormal numbers)
+    out = run(handles[D], d, page, 10 ** 6, D ** -0.5)
+    d["q"].view(-1, D)[::3] = 0
+    assert worst_error(out, d, 10 ** 6, D ** -0.5)[0] <= 1.0
