@@ -51,6 +51,7 @@
  *     e2m1_rne_satfinite(x * 2^-E); QK^T over the dequantised values, then
  *     the same per-tile softmax, e4m3 P and FP8 V as above.
  */
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
@@ -645,7 +646,9 @@ void or_attn_exact_head(const uint16_t* q, const uint16_t* k, const uint16_t* v,
  *   vsc_j), exact bf16 of dec(v8_j); out = sum_j w_j dec(v8_j) / sum_j p_j.
  * out[T][H][D] bf16. */
 /* The query side of the decode, one (token, head) row: q_hat = fwht(q)
- * (fp32); a = max |q_hat|; s = a/448, r = 448/a (IEEE fp32 divides);
+ * (fp32); a = max |q_hat|; s = a/448, r = 448/a (IEEE fp32 divides; r the
+ * largest finite fp32 where the quotient is not finite, so that an element
+ * of zero keeps code 0);
  * codes[e] = e4m3(fp32(q_hat[e] * r)) ([PA] Changes: Q quantised to the FP8
  * format of the cache, FP8_MAX 448); a == 0 -> s = 0 and codes 0. */
 void or_decode_quant_q_row(const uint16_t* q, int D, uint8_t* codes, float* scale)
@@ -656,7 +659,7 @@ void or_decode_quant_q_row(const uint16_t* q, int D, uint8_t* codes, float* scal
     float a = 0.0f;
     for (int e = 0; e < D; ++e) if (fabsf(qh[e]) > a) a = fabsf(qh[e]);
     float s = 0.0f, r = 0.0f;
-    if (a != 0.0f) { s = a / 448.0f; r = 448.0f / a; }
+    if (a != 0.0f) { s = a / 448.0f; r = fminf(448.0f / a, FLT_MAX); }
     for (int e = 0; e < D; ++e) {
         float y = qh[e] * r;
         codes[e] = (a != 0.0f) ? or_e4m3_encode((double)y) : 0;

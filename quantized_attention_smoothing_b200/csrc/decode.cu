@@ -619,11 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int d = 0; d < kQe; ++d) amax = fmaxf(amax, fabsf(x[d]));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            float s = 0.0f, rr = 0.0f;
-            if (amax != 0.0f) {
-                s = __fdiv_rn(amax, 448.0f);
-                rr = __fdiv_rn(448.0f, amax);
-            }
+            const float s = amax != 0.0f ? __fdiv_rn(amax, 448.0f) : 0.0f, rr = e4m3_inv_scale(amax);
             if (qq == 0) sq[r] = s;
             // the codes and scale also go to the caller's optional outputs
             // (written once, by the first CTA of (b, hk))
