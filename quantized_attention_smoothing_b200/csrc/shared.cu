@@ -883,8 +883,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // unit's sum is checked, the loads measured 4 to 7 % slower)
                 uint32_t x0[32], x1[32];
                 tc_fence_after();
-                tmem_ld32(ts, x0);
-                tmem_ld32(ts + 32, x1);
                 const int key0 = (tb + i) * kKeys + 64 * h;
                 const int badm = meta[c];
                 const float4* ks = reinterpret_cast<const float4*>(scl + c * Sm::kScSlot + 64 * h);
@@ -926,8 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (vexp == kNoExp) vexp = ve;               // (no key before: O holds zeros)
                 const bool none = key_hi < key0 || key_lo > key0 + 63, all = key_lo <= key0 && key_hi >= key0 + 63;
                 bool slow = ve != vexp || badm != 0 || key0 + 63 >= gone || (OWN && key0 < there) || !__all_sync(0xffffffffu, none || all);
-                tmem_wait_ld(x0);
-                tmem_wait_ld(x1);
+                tmem_ld64_wait(ts, x0, x1);
                 auto fast = [&](auto plain) {
                     const uint64_t nsub2 = f2_pack(-m_run, -m_run);
                     uint64_t lu[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};
@@ -967,8 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int cc = 0; cc < 2; ++cc) {
                         uint32_t x[32];
-                        tmem_ld32(ts + 32 * cc, x);
-                        tmem_wait_ld(x);
+                        tmem_ld32_wait(ts + 32 * cc, x);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
                             scaled(tensor, x, cc, q, y[16 * cc + 2 * q], y[16 * cc + 2 * q + 1]);
@@ -1066,8 +1062,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int hf = 0; hf < D / 32; ++hf) {
                     uint32_t o[32];
-                    tmem_ld32(to + 32 * hf, o);
-                    tmem_wait_ld(o);
+                    tmem_ld32_wait(to + 32 * hf, o);
                     float y[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(o[j]) * unit;
@@ -1088,8 +1083,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int hf = 0; hf < D / 64; ++hf) {
                     uint32_t o[32];
-                    tmem_ld32(to + give + 32 * hf, o);
-                    tmem_wait_ld(o);
+                    tmem_ld32_wait(to + give + 32 * hf, o);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) xo[(give + 32 * hf + j) * 128 + r] = __uint_as_float(o[j]) * unit;
                 }
@@ -1104,8 +1098,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int hf = 0; hf < D / 64; ++hf) {
                     uint32_t o[32];
-                    tmem_ld32(to + keep + 32 * hf, o);
-                    tmem_wait_ld(o);
+                    tmem_ld32_wait(to + keep + 32 * hf, o);
                     float y[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
