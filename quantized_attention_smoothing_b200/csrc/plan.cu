@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(const PlanParams p) {
         // (a copy onto itself where the outputs are the inputs' buffers)
         for (int b = gtid; b < p.B; b += nthr) p.ctx[b] = p.cached[b];
         for (int b = gtid; b <= p.B; b += nthr) p.offsets[b] = 0;
-        for (int t = gtid; t < p.max_tokens; t += nthr) p.slots[t] = -1;
+        // (64-bit: a slot map may be as long as a 32-bit length says)
+        for (int64_t t = gtid; t < p.max_tokens; t += nthr) p.slots[t] = -1;
         if (gtid == 0) *p.free_count_out = fc;
         return;
     }
