@@ -478,7 +478,9 @@ sage_status sage_page_plan(const int32_t* cached_lens, const int32_t* new_lens, 
  * page_size]. With SAGE_KV_PER_TENSOR_SCALES k_scale / v_scale point to one
  * positive fp32 each, which is read: code = e4m3_rn_sat(x * (1 / scale)).
  * Caches and SAGE_KV_V_TRANSPOSED as for sage_attn_decode, 16-byte aligned.
- * Nothing but the slots' own bytes is written. */
+ * Nothing but the slots' own bytes is written. An element that is not finite
+ * spoils its own row (token and head) alone: an infinite one makes the scale
+ * infinite and its own code NaN, a NaN stays one (and is no part of a). */
 sage_status sage_kv_append(sage_hadamard h, sage_cview4 k_bf16, sage_cview4 v_bf16, const float* k_mean,
                            const int32_t* slot_map, uint8_t* k_cache, uint8_t* v_cache, float* k_scale,
                            float* v_scale, int page_size, int num_pages, int kv_flags, void* stream);
@@ -487,7 +489,9 @@ sage_status sage_kv_append(sage_hadamard h, sage_cview4 k_bf16, sage_cview4 v_bf
  * 128): per 32 consecutive elements a = max|x|, E = floor(log2 a) - 2 clamped
  * to [-127, 125] (-127 for a = 0 or subnormal), codes E2M1(x * 2^-E) rounded
  * to nearest even and saturating, scale byte E + 127 (sage_quant_qk_mx's
- * block format). */
+ * block format). The format has no infinity and no NaN: an infinite element
+ * makes E = 125 and is held as 6 * 2^125 with its sign, a NaN (no part of a) as
+ * some number of its block's range. */
 sage_status sage_kv_append_mxfp4(sage_hadamard h, sage_cview4 k_bf16, sage_cview4 v_bf16,
                                  const float* k_mean, const int32_t* slot_map, uint8_t* k_cache,
                                  uint8_t* v_cache, uint8_t* k_sf, uint8_t* v_sf, int page_size,

@@ -94,7 +94,7 @@ __device__ __forceinline__ uint2 codes_e4m3(const uint64_t (&x)[4], float r) {
 // Eight E2M1 codes of an MX block whose largest value is a; sf: its e8m0 byte.
 __device__ __forceinline__ uint32_t codes_e2m1(const uint64_t (&x)[4], float a, uint32_t& sf) {
     const int ef = static_cast<int>(__float_as_uint(a) >> 23);            // a >= +0
-    const int E = ef == 0 ? -127 : max(ef - 129, -127);
+    const int E = ef == 0 ? -127 : min(max(ef - 129, -127), 125);         // (infinite a: as the largest finite)
     const float sc = __uint_as_float(static_cast<uint32_t>(127 - E) << 23);   // 2^-E
     const uint64_t s2 = p2(sc, sc);
     sf = static_cast<uint32_t>(E + 127);
