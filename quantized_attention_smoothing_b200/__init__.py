@@ -170,6 +170,34 @@ def _bytes(t):
     return 0 if t is None else t.numel() * t.element_size()
 
 
+# The serving entry points write where tables and slots say, and the C ABI sees
+# pointers alone, so their bindings hold every tensor against the call's sizes.
+# Reading an attribute of a tensor takes some 60 ns, so each binding reads what
+# it needs in one condition, and _refuse looks for the tensor when it fails.
+
+def _refuse(where, device, *specs):
+    """ValueError for the first of (name, tensor, dtype, elements) that is not
+    a contiguous tensor of that type, with so many elements, on the device; the
+    library's own refusal of a null pointer for None."""
+    for what, t, dtype, n in specs:
+        if t is None:
+            raise SageError(SAGE_ERR_INVALID_ARG, where)
+        right = t.itemsize == 1 if dtype is torch.uint8 else t.dtype is dtype
+        if not (right and t.numel() >= n and t.is_contiguous() and t.get_device() == device):
+            raise ValueError("%s: expected at least %d contiguous elements of %s on device %d, got %s of shape %s, "
+                             "strides %s on %s" % (what, n, dtype, device, t.dtype, tuple(t.shape), t.stride(), t.device))
+
+
+def _refuse_views(device, *views):
+    for what, t in views:
+        if t.dtype is not torch.bfloat16 or t.get_device() != device:
+            raise ValueError("%s: expected bfloat16 on device %d, got %s on %s" % (what, device, t.dtype, t.device))
+
+
+def _device():
+    return torch._C._cuda_getDevice()
+
+
 def _stream(stream):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
@@ -363,23 +391,59 @@ def _shared_ws(q, Hk, ws, stream):
     return ws
 
 
+def _check_shared(where, h, q, out, k_cache, v_cache, k_scale, v_scale, kind, scales, tokens, width, prefix_table, prefix_len,
+                  page_table, ctx_lens, ws, rows):
+    """The checks of both forms of the shared decode; `scales` elements of
+    `kind`, `tokens` rows of `width` bytes."""
+    dev, i32, B = h.device, torch.int32, q.shape[0]
+    try:
+        if (rows >= B and q.dtype is out.dtype is torch.bfloat16
+                and prefix_table.dtype is prefix_len.dtype is page_table.dtype is ctx_lens.dtype is i32
+                and dev == q.get_device() == out.get_device() == k_cache.get_device() == v_cache.get_device()
+                == k_scale.get_device() == v_scale.get_device() == prefix_table.get_device() == prefix_len.get_device()
+                == page_table.get_device() == ctx_lens.get_device() == ws.get_device()
+                and k_cache.itemsize == v_cache.itemsize == 1
+                and k_cache.nbytes >= tokens * width <= v_cache.nbytes
+                and k_scale.dtype is v_scale.dtype is kind and k_scale.numel() >= scales <= v_scale.numel()
+                and ctx_lens.numel() >= B
+                and k_cache.is_contiguous() and v_cache.is_contiguous() and prefix_table.is_contiguous()
+                and page_table.is_contiguous() and ctx_lens.is_contiguous()
+                and k_scale.is_contiguous() and v_scale.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    _refuse_views(dev, ("q", q), ("out", out))
+    _refuse(where, dev, ("k_cache", k_cache, torch.uint8, tokens * width), ("v_cache", v_cache, torch.uint8, tokens * width),
+            ("k scales", k_scale, kind, scales), ("v scales", v_scale, kind, scales),
+            ("prefix_table", prefix_table, i32, 0), ("prefix_len", prefix_len, i32, 1),
+            ("page_table", page_table, i32, B * page_table.shape[1]), ("ctx_lens", ctx_lens, i32, B),
+            ("ws", ws, torch.uint8, 0))
+
+
 def sage_attn_decode_shared(h, q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_len,
                             page_table, ctx_lens, page_size, num_pages, window, softmax_scale, out,
                             ws=None, stream=None, kv_flags=0):
     """sage_attn_decode for a batch whose sequences begin with the same tokens:
     prefix_table int32 [pages] and prefix_len int32 [1] (both on the GPU)
     give the shared tokens' pages, page_table [B, max_pages] and ctx_lens
-    count from the sequence's first token as in sage_attn_decode."""
+    count from the sequence's first token as in sage_attn_decode. Tensors of
+    another type, device or layout, or smaller than the call's sizes, raise
+    ValueError."""
     B, T, H, D = q.shape
     Hk = k_cache.shape[1]
+    rows, max_pages = page_table.shape
+    page_size, num_pages, kv_flags = int(page_size), int(num_pages), int(kv_flags)
     ws = _shared_ws(q, Hk, ws, stream)
-    _check(lib().sage_attn_decode_shared(h.handle, _view(q, CView4), _ptr(k_cache), _ptr(v_cache),
-                                         _ptr(k_scale), _ptr(v_scale), _ptr(prefix_table),
-                                         prefix_table.numel(), _ptr(prefix_len), _ptr(page_table),
-                                         _ptr(ctx_lens), B, T, H, Hk, D, int(page_size),
-                                         int(page_table.shape[1]), int(num_pages), int(window),
-                                         float(softmax_scale), int(kv_flags), _view(out, View4), _ptr(ws),
-                                         _bytes(ws), _stream(stream)),
+    tokens = num_pages * Hk * page_size
+    _check_shared("sage_attn_decode_shared", h, q, out, k_cache, v_cache, k_scale, v_scale, torch.float32,
+                  1 if kv_flags & SAGE_KV_PER_TENSOR_SCALES else tokens, tokens, D, prefix_table, prefix_len, page_table,
+                  ctx_lens, ws, rows)
+    _check(lib().sage_attn_decode_shared(h.handle, _view(q, CView4), k_cache.data_ptr(),
+                                         v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                         prefix_table.data_ptr(), prefix_table.numel(), prefix_len.data_ptr(),
+                                         page_table.data_ptr(), ctx_lens.data_ptr(), B, T, H, Hk, D, page_size,
+                                         max_pages, num_pages, int(window), float(softmax_scale), kv_flags, _view(out, View4), ws.data_ptr(),
+                                         ws.nbytes, _stream(stream)),
            "sage_attn_decode_shared")
 
 
@@ -390,14 +454,18 @@ def sage_attn_decode_shared_mxfp4(h, q, k_cache, v_cache, k_sf, v_sf, prefix_tab
     sage_attn_decode_mxfp4)."""
     B, T, H, D = q.shape
     Hk = k_cache.shape[1]
+    rows, max_pages = page_table.shape
+    page_size, num_pages = int(page_size), int(num_pages)
     ws = _shared_ws(q, Hk, ws, stream)
-    _check(lib().sage_attn_decode_shared_mxfp4(h.handle, _view(q, CView4), _ptr(k_cache), _ptr(v_cache),
-                                               _ptr(k_sf), _ptr(v_sf), _ptr(prefix_table),
-                                               prefix_table.numel(), _ptr(prefix_len), _ptr(page_table),
-                                               _ptr(ctx_lens), B, T, H, Hk, D, int(page_size),
-                                               int(page_table.shape[1]), int(num_pages), int(window),
-                                               float(softmax_scale), _view(out, View4), _ptr(ws),
-                                               _bytes(ws), _stream(stream)),
+    tokens = num_pages * Hk * page_size
+    _check_shared("sage_attn_decode_shared_mxfp4", h, q, out, k_cache, v_cache, k_sf, v_sf, torch.uint8, tokens * D // 32, tokens, D // 2, prefix_table,
+                  prefix_len, page_table, ctx_lens, ws, rows)
+    _check(lib().sage_attn_decode_shared_mxfp4(h.handle, _view(q, CView4), k_cache.data_ptr(),
+                                               v_cache.data_ptr(), k_sf.data_ptr(), v_sf.data_ptr(),
+                                               prefix_table.data_ptr(), prefix_table.numel(), prefix_len.data_ptr(),
+                                               page_table.data_ptr(), ctx_lens.data_ptr(), B, T, H, Hk, D,
+                                               page_size, max_pages, num_pages, int(window), float(softmax_scale), _view(out, View4), ws.data_ptr(),
+                                               ws.nbytes, _stream(stream)),
            "sage_attn_decode_shared_mxfp4")
 
 
@@ -405,39 +473,97 @@ def sage_page_plan(cached_lens, new_lens, free_list, free_count, page_size, page
                    free_count_out, token_offsets, slot_map, prefix_table=None, stream=None):
     """Block tables, the free list and the new tokens' slots of one serving
     step (all int32 tensors; ctx_lens may be cached_lens and free_count_out
-    free_count)."""
+    free_count). Tensors of another type, device or layout, or shorter than
+    page_table's rows say, raise ValueError."""
     B, max_pages = page_table.shape
-    _check(lib().sage_page_plan(_ptr(cached_lens), _ptr(new_lens), _ptr(prefix_table),
-                                0 if prefix_table is None else prefix_table.numel(), _ptr(free_list),
-                                _ptr(free_count), B, max_pages, int(page_size), free_list.numel(),
-                                0 if slot_map is None else slot_map.numel(), _ptr(page_table),
-                                _ptr(ctx_lens), _ptr(free_count_out), _ptr(token_offsets),
+    i32, dev = torch.int32, _device()
+    try:
+        right = (cached_lens.dtype is new_lens.dtype is free_list.dtype is free_count.dtype is page_table.dtype
+                 is ctx_lens.dtype is free_count_out.dtype is token_offsets.dtype is i32
+                 and dev == cached_lens.get_device() == new_lens.get_device() == free_list.get_device()
+                 == free_count.get_device() == page_table.get_device() == ctx_lens.get_device()
+                 == free_count_out.get_device() == token_offsets.get_device()
+                 and cached_lens.numel() >= B <= new_lens.numel() and ctx_lens.numel() >= B < token_offsets.numel()
+                 and cached_lens.is_contiguous() and new_lens.is_contiguous() and free_list.is_contiguous()
+                 and page_table.is_contiguous() and ctx_lens.is_contiguous() and token_offsets.is_contiguous()
+                 and (slot_map is None or slot_map.dtype is i32 and slot_map.get_device() == dev
+                      and slot_map.is_contiguous())
+                 and (prefix_table is None or prefix_table.dtype is i32 and prefix_table.get_device() == dev
+                      and prefix_table.is_contiguous()))
+    except AttributeError:
+        right = False
+    if not right:
+        _refuse("sage_page_plan", dev, ("cached_lens", cached_lens, i32, B), ("new_lens", new_lens, i32, B), ("free_list", free_list, i32, 0),
+                ("free_count", free_count, i32, 1), ("page_table", page_table, i32, 0), ("ctx_lens", ctx_lens, i32, B),
+                ("free_count_out", free_count_out, i32, 1), ("token_offsets", token_offsets, i32, B + 1),
+                *((n, t, i32, 0) for n, t in (("slot_map", slot_map), ("prefix_table", prefix_table)) if t is not None))
+    _check(lib().sage_page_plan(cached_lens.data_ptr(), new_lens.data_ptr(), _ptr(prefix_table),
+                                0 if prefix_table is None else prefix_table.numel(), free_list.data_ptr(),
+                                free_count.data_ptr(), B, max_pages, int(page_size), free_list.numel(),
+                                0 if slot_map is None else slot_map.numel(), page_table.data_ptr(),
+                                ctx_lens.data_ptr(), free_count_out.data_ptr(), token_offsets.data_ptr(),
                                 _ptr(slot_map), _stream(stream)), "sage_page_plan")
 
 
-def _tokens_view(t):
+def _tokens_view(t, shape):
     """[N, Hk, D] as the [1, N, Hk, D] view of the C ABI."""
-    if t.dim() != 3:
-        raise ValueError("expected [tokens, heads, head size], got shape %s" % (tuple(t.shape),))
-    return CView4.from_buffer_copy(_pack_view(t.data_ptr(), 1, *t.shape, 0, *t.stride()))
+    return CView4.from_buffer_copy(_pack_view(t.data_ptr(), 1, *shape, 0, *t.stride()))
+
+
+def _check_append(where, h, k, v, shape, slot_map, k_cache, v_cache, cache, k_scale, v_scale, k_mean, kind, scales, packed):
+    """The checks of both forms of the cache write: tokens of `shape` = [N, Hk,
+    D], a K cache of shape `cache` = [num_pages, Hk, page, D / packed]."""
+    if len(shape) != 3 or v.dim() != 3:
+        raise ValueError("expected [tokens, heads, head size], got shapes %s and %s" % (tuple(shape), tuple(v.shape)))
+    N, Hk, D = shape
+    if N == 0:                                            # (nothing is read or written)
+        return
+    dev, i32 = h.device, torch.int32
+    if len(cache) != 4 or cache[1] != Hk or cache[3] * packed != D:
+        raise ValueError("k_cache: shape %s for tokens of %d heads of %d" % (tuple(cache), Hk, D))
+    try:
+        if (k.dtype is v.dtype is torch.bfloat16 and k_scale.dtype is v_scale.dtype is kind
+                and slot_map.dtype is i32 and k_cache.itemsize == v_cache.itemsize == 1
+                and dev == k.get_device() == v.get_device() == slot_map.get_device() == k_cache.get_device()
+                == v_cache.get_device() == k_scale.get_device() == v_scale.get_device()
+                and slot_map.numel() >= N and v_cache.nbytes >= k_cache.nbytes
+                and k_scale.numel() >= scales <= v_scale.numel()
+                and slot_map.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous()
+                and k_scale.is_contiguous() and v_scale.is_contiguous()
+                and (k_mean is None or k_mean.dtype is torch.float32 and k_mean.numel() >= Hk * D
+                     and k_mean.is_contiguous() and k_mean.get_device() == dev)):
+            return
+    except AttributeError:
+        pass
+    _refuse_views(dev, ("k", k), ("v", v))
+    _refuse(where, dev, ("slot_map", slot_map, i32, N), ("k_cache", k_cache, torch.uint8, 0),
+            ("v_cache", v_cache, torch.uint8, k_cache.numel()), ("k scales", k_scale, kind, scales),
+            ("v scales", v_scale, kind, scales),
+            *(() if k_mean is None else (("k_mean", k_mean, torch.float32, Hk * D),)))
 
 
 def sage_kv_append(h, k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_mean=None, kv_flags=0,
                    stream=None):
     """Quantise the new tokens' k and v ([N, Hk, D] bf16 views) into an FP8
-    cache at slot_map (int32 [N]; a negative slot skips its token)."""
-    _check(lib().sage_kv_append(h.handle, _tokens_view(k), _tokens_view(v), _ptr(k_mean), _ptr(slot_map),
-                                _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                                int(k_cache.shape[2]), int(k_cache.shape[0]), int(kv_flags),
-                                _stream(stream)), "sage_kv_append")
+    cache [num_pages, Hk, page, D] at slot_map (int32 [N]; a negative slot skips
+    its token). Tensors of another type, device or layout, or too small, raise
+    ValueError."""
+    shape, cache = k.shape, k_cache.shape
+    _check_append("sage_kv_append", h, k, v, shape, slot_map, k_cache, v_cache, cache, k_scale, v_scale, k_mean, torch.float32,
+                  1 if kv_flags & SAGE_KV_PER_TENSOR_SCALES else cache[0] * cache[1] * cache[2], 1)
+    _check(lib().sage_kv_append(h.handle, _tokens_view(k, shape), _tokens_view(v, v.shape), _ptr(k_mean),
+                                _ptr(slot_map), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                v_scale.data_ptr(), cache[2], cache[0], int(kv_flags), _stream(stream)), "sage_kv_append")
 
 
 def sage_kv_append_mxfp4(h, k, v, slot_map, k_cache, v_cache, k_sf, v_sf, k_mean=None, stream=None):
     """sage_kv_append into an MXFP4 cache (the layouts of sage_attn_decode_mxfp4)."""
-    _check(lib().sage_kv_append_mxfp4(h.handle, _tokens_view(k), _tokens_view(v), _ptr(k_mean),
-                                      _ptr(slot_map), _ptr(k_cache), _ptr(v_cache), _ptr(k_sf), _ptr(v_sf),
-                                      int(k_cache.shape[2]), int(k_cache.shape[0]), _stream(stream)),
-           "sage_kv_append_mxfp4")
+    shape, cache = k.shape, k_cache.shape
+    _check_append("sage_kv_append_mxfp4", h, k, v, shape, slot_map, k_cache, v_cache, cache, k_sf, v_sf, k_mean, torch.uint8,
+                  k_cache.numel() // 16, 2)
+    _check(lib().sage_kv_append_mxfp4(h.handle, _tokens_view(k, shape), _tokens_view(v, v.shape), _ptr(k_mean),
+                                      _ptr(slot_map), k_cache.data_ptr(), v_cache.data_ptr(), k_sf.data_ptr(),
+                                      v_sf.data_ptr(), cache[2], cache[0], _stream(stream)), "sage_kv_append_mxfp4")
 
 
 def sage_quant_qk_mx(h, q, k, q4, q_sf, k4, k_sf, k_mean=None, ws=None, stream=None):
