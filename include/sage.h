@@ -394,7 +394,8 @@ size_t sage_attn_decode_shared_workspace(int B, int T, int H, int Hk, int D);
  * results of the two parts are combined in fp32 (log-sum-exp). The weights,
  * and with an FP8 cache the scaled values, are held in fp16 where
  * sage_attn_decode holds them in bf16, relative to the largest v_scale a run
- * of keys has had: values whose v_scale is below 2^-16 of it lose bits. Slots
+ * of keys has had: a v_scale below 2^-13 of it has fewer than fp16's 11 bits
+ * (it is off by at most 2^-24 of the largest one). Slots
  * that hold no key of [0, ctx) may hold any bytes, scales included. The other
  * arguments, cache formats, limits and errors are sage_attn_decode's; also
  * UNSUPPORTED: B * Hk > 65535, B * T * H or a table of 2^31 or more tokens.

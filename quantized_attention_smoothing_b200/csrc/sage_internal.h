@@ -163,7 +163,7 @@ struct DecodeArgs {
 size_t decode_ws_bytes(int B, int T, int H, int Hk, int D, int window);
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t s);
 unsigned read_clear_decode_error();
-unsigned read_clear_decode_error();
+
 // ---- decode of a batch that shares a prefix (shared.cu)
 struct DecodeSharedArgs {
     DecodeArgs d;

@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(128) query_kernel(const QueryParams p) {
 
 // CTA = 16 warps:
 //   warps 0-7   softmax, two groups of four; thread = one query row (TMEM lane)
-//               and all 128 keys of a unit, so the row statistics need no
+//               and all 64 keys of a unit, so the row statistics need no
 //               shuffles;
 //   warps 8-11  V converters: e4m3 -> fp16, the value's scale multiplied in
 //               (MXFP4: K and V -> bf16, exactly);
@@ -445,7 +445,7 @@ struct SmP {
     static constexpr int kVsf = kKsf + kStages * kSfStage;
     static constexpr int kKb = MX ? al1024(kVsf + kStages * kSfStage) : kVsf;
     static constexpr int kKbBuf = MX ? kKeys * 2 * D : 0;
-    static constexpr int kVb = kKb + kKbBuf;                         // [2] bf16 V, D / 64 atoms [128][128 B]
+    static constexpr int kVb = kKb + kKbBuf;                         // [2] V, fp16 (MX: bf16), D / 64 atoms [128][128 B]
     static constexpr int kVbBuf = kKeys * 2 * D;
     static constexpr int kScale = kVb + 2 * kVbBuf;                  // [slot] k [128] fp32, v [128] fp16
     static constexpr int kScSlot = MX ? 0 : kKeys + kKeys / 2;
@@ -467,9 +467,9 @@ struct SmP {
     static_assert(kBytes + 1024 <= 227 * 1024, "shared memory");
 };
 
-// D[tmem] (+)= A[tmem] * B[smem], bf16 x bf16 -> fp32 (A: lane = row, a
-// 32-bit column two consecutive keys).
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+// D[tmem] (+)= A[tmem] * B[smem], fp16 or bf16 (both operands the same, as idesc
+// says) -> fp32 (A: lane = row, a 32-bit column two consecutive keys).
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -835,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int st = 0; st < 4; ++st)
-                            mma_bf16_ts(to, ts + 64 * h + 8 * st, vd + st * vstep, idesc_pv,
+                            mma_f16_ts(to, ts + 64 * h + 8 * st, vd + st * vstep, idesc_pv,
                                         (j > 0 || h > 0 || st > 0) ? 1u : 0u);
                         mma_commit(pv_done + h);
                         if (h == 1) mma_commit(&bars[Sm::kVFree + vb]);
