@@ -130,15 +130,24 @@ def plan(a):
                         a["free_count_out"], a["token_offsets"], a["slot_map"], prefix_table=a["prefix_table"])
 
 
-@pytest.mark.parametrize("how", ["type", "short", "strided", "expanded", "device"])
-@pytest.mark.parametrize("name", list(PLAN_ARGS))
+HOW = ["type", "device", "short", "strided", "expanded"]
+
+
+def cases(names, unless):
+    """Every (name, how) but those that are not the binding's to refuse: a name's
+    own length may be the call's, a single element has no layout, views any."""
+    return [(n, how) for n in names for how in HOW if how not in unless.get(n, ())]
+
+
+SHORT, LAYOUT = ("short",), ("short", "strided", "expanded")
+
+
+@pytest.mark.parametrize("name,how", cases(PLAN_ARGS, dict(free_list=SHORT, slot_map=SHORT, prefix_table=SHORT,
+                                                           page_table=SHORT, free_count=LAYOUT, free_count_out=LAYOUT)))
 def test_plan_binding_refuses(on_cpu, name, how):
     a = {n: i32(*s) for n, s in PLAN_ARGS.items()}
     plan(a)
     n = len(on_cpu.calls)
-    whole = {"free_list", "slot_map", "prefix_table", "page_table"}      # their own lengths are the call's
-    if how == "short" and name in whole or how in ("short", "strided", "expanded") and a[name].numel() == 1:
-        pytest.skip("not wrong")
     with pytest.raises(ValueError, match=name):
         plan({**a, name: wrong(a[name], how)})
     assert len(on_cpu.calls) == n
@@ -168,16 +177,13 @@ def append(mx, a, tensor=False):
       **({} if mx else dict(kv_flags=1 if tensor else 0)))
 
 
-@pytest.mark.parametrize("how", ["type", "short", "strided", "expanded", "device"])
-@pytest.mark.parametrize("name", ["k", "v", "slot_map", "k_cache", "v_cache", "k scales", "v scales", "k_mean"])
+@pytest.mark.parametrize("name,how", cases(["k", "v", "slot_map", "k_cache", "v_cache", "k scales", "v scales", "k_mean"],
+                                           dict(k=LAYOUT, v=LAYOUT, k_cache=SHORT)))
 @pytest.mark.parametrize("mx", [False, True])
 def test_append_binding_refuses(on_cpu, mx, name, how):
     a = append_tensors(mx)
     append(mx, a)
     n = len(on_cpu.calls)
-    # views may have any strides, their sizes are the call's; so are the K cache's
-    if name in ("k", "v") and how in ("short", "strided", "expanded") or name == "k_cache" and how == "short":
-        pytest.skip("not the binding's to refuse")
     with pytest.raises(ValueError, match=name):
         append(mx, {**a, name: wrong(a[name], how)})
     assert len(on_cpu.calls) == n
@@ -214,17 +220,14 @@ SHARED_NAMES = {"q": "q", "out": "out", "k_cache": "k_cache", "v_cache": "v_cach
                 "length": "prefix_len", "table": "page_table", "ctx": "ctx_lens", 0: "k scales", 1: "v scales", "ws": "ws"}
 
 
-@pytest.mark.parametrize("how", ["type", "short", "strided", "expanded", "device"])
-@pytest.mark.parametrize("key", list(SHARED_NAMES))
+@pytest.mark.parametrize("key,how", cases(SHARED_NAMES, dict(q=LAYOUT, out=LAYOUT, prefix=SHORT, length=LAYOUT,
+                                                             ws=("type",) + LAYOUT)))
 @pytest.mark.parametrize("mx", [False, True])
 def test_shared_binding_refuses(on_cpu, mx, key, how):
     name = "sage_attn_decode_shared" + ("_mxfp4" if mx else "")
     a = dict(attend_args(mx=mx), ws=torch.zeros(4096, dtype=torch.uint8))
     attend(name, a, ws=a["ws"])
     n = len(on_cpu.calls)
-    if key in ("q", "out") and how in ("short", "strided", "expanded") or key == "prefix" and how == "short" \
-            or key == "length" and how in ("short", "strided", "expanded") or key == "ws" and how != "device":
-        pytest.skip("not the binding's to refuse")
     b = dict(a, scales=list(a["scales"]))
     if key in (0, 1):
         b["scales"][key] = wrong(b["scales"][key], how)
