@@ -471,8 +471,8 @@ sage_status sage_page_plan(const int32_t* cached_lens, const int32_t* new_lens, 
  *   slot_map: int32 [N], token n's slot page * page_size + offset; a negative
  *   slot skips its token; a slot >= num_pages * page_size is skipped and
  *   reported by sage_device_error as INVALID_ARG (kernel SAGE_KERNEL_APPEND).
- *   Slots of one call must differ: of tokens that share one, which one's
- *   codes and scales stay is not specified.
+ *   Slots of one call must differ: what a slot holds that several tokens
+ *   share is not specified (codes of one and a scale of another, even).
  * Per token and head: x = butterfly(K - k_mean) for K, x = V for V;
  * a = max|x|, scale = a / 448, code = e4m3_rn_sat(x * (448 / a)) (a = 0:
  * scale 0 and zero codes), written to k_scale / v_scale [num_pages, Hk,
@@ -504,10 +504,11 @@ const char* sage_status_string(sage_status s);
 /* Synchronise `stream`, then read and clear the library's device error
  * words on the current device: SAGE_ERR_TIMEOUT if a bounded wait expired
  * since the last call, SAGE_ERR_CUDA if the stream reports a CUDA error,
- * SAGE_ERR_INVALID_ARG if sage_attn_decode met device-side arguments out of
- * range (a context length above max_pages * page_size, clamped; or a page id
- * outside [0, num_pages) for a page holding keys of a window, whose keys were
- * then left out), SAGE_OK otherwise. */
+ * SAGE_ERR_INVALID_ARG if a decode met device-side arguments out of range (a
+ * context length above max_pages * page_size, or a prefix length, clamped; or a
+ * page id outside [0, num_pages) for a page holding keys of a window, whose
+ * keys were then left out), a page plan was refused or a cache write met a slot
+ * off the cache, SAGE_OK otherwise. */
 sage_status sage_device_error(void* stream);
 
 /* Kernel ids reported by sage_device_error_where. */
