@@ -391,8 +391,8 @@ def _shared_ws(q, Hk, ws, stream):
     return ws
 
 
-def _check_shared(where, h, q, out, k_cache, v_cache, k_scale, v_scale, kind, scales, tokens, width, prefix_table, prefix_len,
-                  page_table, ctx_lens, ws, rows):
+def _check_shared(where, h, q, out, k_cache, v_cache, k_scale, v_scale, kind, scales, tokens, width,
+                  prefix_table, prefix_len, page_table, ctx_lens, ws, rows):
     """The checks of both forms of the shared decode; `scales` elements of
     `kind`, `tokens` rows of `width` bytes."""
     dev, i32, B = h.device, torch.int32, q.shape[0]
@@ -413,7 +413,8 @@ def _check_shared(where, h, q, out, k_cache, v_cache, k_scale, v_scale, kind, sc
     except AttributeError:
         pass
     _refuse_views(dev, ("q", q), ("out", out))
-    _refuse(where, dev, ("k_cache", k_cache, torch.uint8, tokens * width), ("v_cache", v_cache, torch.uint8, tokens * width),
+    _refuse(where, dev, ("k_cache", k_cache, torch.uint8, tokens * width),
+            ("v_cache", v_cache, torch.uint8, tokens * width),
             ("k scales", k_scale, kind, scales), ("v scales", v_scale, kind, scales),
             ("prefix_table", prefix_table, i32, 0), ("prefix_len", prefix_len, i32, 1),
             ("page_table", page_table, i32, B * page_table.shape[1]), ("ctx_lens", ctx_lens, i32, B),
@@ -442,8 +443,8 @@ def sage_attn_decode_shared(h, q, k_cache, v_cache, k_scale, v_scale, prefix_tab
                                          v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                          prefix_table.data_ptr(), prefix_table.numel(), prefix_len.data_ptr(),
                                          page_table.data_ptr(), ctx_lens.data_ptr(), B, T, H, Hk, D, page_size,
-                                         max_pages, num_pages, int(window), float(softmax_scale), kv_flags, _view(out, View4), ws.data_ptr(),
-                                         ws.nbytes, _stream(stream)),
+                                         max_pages, num_pages, int(window), float(softmax_scale), kv_flags,
+                                         _view(out, View4), ws.data_ptr(), ws.nbytes, _stream(stream)),
            "sage_attn_decode_shared")
 
 
@@ -458,14 +459,14 @@ def sage_attn_decode_shared_mxfp4(h, q, k_cache, v_cache, k_sf, v_sf, prefix_tab
     page_size, num_pages = int(page_size), int(num_pages)
     ws = _shared_ws(q, Hk, ws, stream)
     tokens = num_pages * Hk * page_size
-    _check_shared("sage_attn_decode_shared_mxfp4", h, q, out, k_cache, v_cache, k_sf, v_sf, torch.uint8, tokens * D // 32, tokens, D // 2, prefix_table,
-                  prefix_len, page_table, ctx_lens, ws, rows)
+    _check_shared("sage_attn_decode_shared_mxfp4", h, q, out, k_cache, v_cache, k_sf, v_sf, torch.uint8,
+                  tokens * D // 32, tokens, D // 2, prefix_table, prefix_len, page_table, ctx_lens, ws, rows)
     _check(lib().sage_attn_decode_shared_mxfp4(h.handle, _view(q, CView4), k_cache.data_ptr(),
                                                v_cache.data_ptr(), k_sf.data_ptr(), v_sf.data_ptr(),
                                                prefix_table.data_ptr(), prefix_table.numel(), prefix_len.data_ptr(),
                                                page_table.data_ptr(), ctx_lens.data_ptr(), B, T, H, Hk, D,
-                                               page_size, max_pages, num_pages, int(window), float(softmax_scale), _view(out, View4), ws.data_ptr(),
-                                               ws.nbytes, _stream(stream)),
+                                               page_size, max_pages, num_pages, int(window), float(softmax_scale),
+                                               _view(out, View4), ws.data_ptr(), ws.nbytes, _stream(stream)),
            "sage_attn_decode_shared_mxfp4")
 
 
@@ -493,8 +494,9 @@ def sage_page_plan(cached_lens, new_lens, free_list, free_count, page_size, page
     except AttributeError:
         right = False
     if not right:
-        _refuse("sage_page_plan", dev, ("cached_lens", cached_lens, i32, B), ("new_lens", new_lens, i32, B), ("free_list", free_list, i32, 0),
-                ("free_count", free_count, i32, 1), ("page_table", page_table, i32, 0), ("ctx_lens", ctx_lens, i32, B),
+        _refuse("sage_page_plan", dev, ("cached_lens", cached_lens, i32, B), ("new_lens", new_lens, i32, B),
+                ("free_list", free_list, i32, 0), ("free_count", free_count, i32, 1),
+                ("page_table", page_table, i32, 0), ("ctx_lens", ctx_lens, i32, B),
                 ("free_count_out", free_count_out, i32, 1), ("token_offsets", token_offsets, i32, B + 1),
                 *((n, t, i32, 0) for n, t in (("slot_map", slot_map), ("prefix_table", prefix_table)) if t is not None))
     _check(lib().sage_page_plan(cached_lens.data_ptr(), new_lens.data_ptr(), _ptr(prefix_table),
@@ -510,7 +512,8 @@ def _tokens_view(t, shape):
     return CView4.from_buffer_copy(_pack_view(t.data_ptr(), 1, *shape, 0, *t.stride()))
 
 
-def _check_append(where, h, k, v, shape, slot_map, k_cache, v_cache, cache, k_scale, v_scale, k_mean, kind, scales, packed):
+def _check_append(where, h, k, v, shape, slot_map, k_cache, v_cache, cache, k_scale, v_scale, k_mean, kind,
+                  scales, packed):
     """The checks of both forms of the cache write: tokens of `shape` = [N, Hk,
     D], a K cache of shape `cache` = [num_pages, Hk, page, D / packed]."""
     if len(shape) != 3 or v.dim() != 3:
@@ -549,8 +552,8 @@ def sage_kv_append(h, k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_mean
     its token). Tensors of another type, device or layout, or too small, raise
     ValueError."""
     shape, cache = k.shape, k_cache.shape
-    _check_append("sage_kv_append", h, k, v, shape, slot_map, k_cache, v_cache, cache, k_scale, v_scale, k_mean, torch.float32,
-                  1 if kv_flags & SAGE_KV_PER_TENSOR_SCALES else cache[0] * cache[1] * cache[2], 1)
+    _check_append("sage_kv_append", h, k, v, shape, slot_map, k_cache, v_cache, cache, k_scale, v_scale, k_mean,
+                  torch.float32, 1 if kv_flags & SAGE_KV_PER_TENSOR_SCALES else cache[0] * cache[1] * cache[2], 1)
     _check(lib().sage_kv_append(h.handle, _tokens_view(k, shape), _tokens_view(v, v.shape), _ptr(k_mean),
                                 _ptr(slot_map), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                                 v_scale.data_ptr(), cache[2], cache[0], int(kv_flags), _stream(stream)), "sage_kv_append")
@@ -559,8 +562,8 @@ def sage_kv_append(h, k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_mean
 def sage_kv_append_mxfp4(h, k, v, slot_map, k_cache, v_cache, k_sf, v_sf, k_mean=None, stream=None):
     """sage_kv_append into an MXFP4 cache (the layouts of sage_attn_decode_mxfp4)."""
     shape, cache = k.shape, k_cache.shape
-    _check_append("sage_kv_append_mxfp4", h, k, v, shape, slot_map, k_cache, v_cache, cache, k_sf, v_sf, k_mean, torch.uint8,
-                  k_cache.numel() // 16, 2)
+    _check_append("sage_kv_append_mxfp4", h, k, v, shape, slot_map, k_cache, v_cache, cache, k_sf, v_sf, k_mean,
+                  torch.uint8, k_cache.numel() // 16, 2)
     _check(lib().sage_kv_append_mxfp4(h.handle, _tokens_view(k, shape), _tokens_view(v, v.shape), _ptr(k_mean),
                                       _ptr(slot_map), k_cache.data_ptr(), v_cache.data_ptr(), k_sf.data_ptr(),
                                       v_sf.data_ptr(), cache[2], cache[0], _stream(stream)), "sage_kv_append_mxfp4")
